@@ -31,26 +31,25 @@ def listed():
         _plan("plan_decode_b64", B=64, L=1, page=64, max_pages=512, lo=1024, hi=32768, short=False),
         # prompts of very different lengths admitted at once; the free list runs out before the last
         _plan("plan_prompts_b512", B=512, L=4096, page=64, max_pages=128, lo=0, hi=4000, short=True),
+        # a few requests of a batch end and give their pages back
+        _release("release_b64", B=64, page=64, max_pages=512, hi=4096),
+        # the largest batch shrinks after long prompts
+        _release("release_b512", B=512, page=64, max_pages=256, hi=16384),
         # one token for each request of a batch into a bf16 paged cache: the latency of every decode step
         _rope("rope_decode_b64", B=64, L=1, Hq=32, Hkv=8, D=128, rot=128, axes=1, order="blocks", pairs="half", fmt="bf16", page=64,
               far=32768),
-        # a long image-and-text prompt: three position axes taken in turn
-        _rope("rope_prompt_8192_3axes", B=1, L=8192, Hq=32, Hkv=8, D=128, rot=128, axes=3, order="cycle", pairs="half",
-              fmt="bf16", page=64, far=131072),
-        # ragged chunks into an E4M3 cache, half of each head rotated, neighbouring elements paired
-        _rope("rope_e4m3_ragged", B=8, L=1000, Hq=16, Hkv=2, D=128, rot=64, axes=2, order="blocks", pairs="adjacent",
-              fmt="e4m3", page=128, far=1000003),
-        # a verify step of 16 tokens a request into a q8_0 cache
-        _rope("rope_q8_verify", B=16, L=16, Hq=16, Hkv=4, D=64, rot=64, axes=1, order="blocks", pairs="half", fmt="q8_0", page=64,
-              far=32768),
-        # a single user's small tree on a short context: latency
-        _tree("tree_b1_t8", B=1, Hq=32, Hkv=8, T=8, D=128, lo=500, hi=500, page=64, ragged=False),
+        # a long image-and-text prompt into an E4M3 cache: three position axes taken in turn
+        _rope("rope_prompt_8192_e4m3", B=1, L=8192, Hq=32, Hkv=8, D=128, rot=128, axes=3, order="cycle", pairs="half",
+              fmt="e4m3", page=64, far=131072),
+        # ragged chunks into a q8_0 cache, half of each head rotated, neighbouring elements paired
+        _rope("rope_q8_ragged", B=8, L=1000, Hq=16, Hkv=2, D=128, rot=64, axes=2, order="blocks", pairs="adjacent",
+              fmt="q8_0", page=128, far=1000003),
+        # a single user's small tree on a short context, head dim 64: latency
+        _tree("tree_b1_t8_d64", B=1, Hq=32, Hkv=8, T=8, D=64, lo=500, hi=500, page=64, ragged=False),
         # the serving batch: 64 requests of 1K to 32K rows, 16 drafted tokens each, paged
         _tree("tree_b64_t16_paged", B=64, Hq=32, Hkv=8, T=16, D=128, lo=1024, hi=32768, page=64, ragged=True),
-        # large trees of uneven size, eight query heads a KV head, contiguous caches of head dim 64
-        _tree("tree_b8_t63_d64", B=8, Hq=32, Hkv=4, T=63, D=64, lo=3000, hi=16000, page=0, ragged=True),
-        # head dim 256
-        _tree("tree_b4_t33_d256", B=4, Hq=16, Hkv=8, T=33, D=256, lo=2000, hi=9001, page=128, ragged=False),
+        # large trees of uneven size, eight query heads a KV head, contiguous caches of head dim 256
+        _tree("tree_b8_t63_d256", B=8, Hq=32, Hkv=4, T=63, D=256, lo=3000, hi=16000, page=0, ragged=True),
         # accepted paths of a small batch, contiguous cache
         _commit("commit_b8", B=8, Hkv=8, D=128, T=16, A=5, page=0, rows=512),
         # accepted paths of the serving batch, paged cache
@@ -60,6 +59,10 @@ def listed():
 
 def _plan(name, **kw):
     return {"op": "plan", "name": name, **kw}
+
+
+def _release(name, **kw):
+    return {"op": "release", "name": name, **kw}
 
 
 def _rope(name, **kw):
@@ -91,7 +94,7 @@ def draw(rng):
                          short=rng.random() < 0.5)
         else:
             hi = _log_int(rng, 1, 16384)
-            case = {"op": "release", "name": None, "B": B, "page": page, "max_pages": -(-hi // page), "hi": hi}
+            case = _release(None, B=B, page=page, max_pages=-(-hi // page), hi=hi)
     elif op == "rope":
         D = rng.choice([64, 128, 128, 256])
         fmt = rng.choice(["bf16", "e4m3", "q8_0"]) if D < 256 else "bf16"
@@ -342,9 +345,10 @@ def _plain_plan(st):
     case, page, table = st["case"], st["case"]["page"], st["table"]
     old, new = st["seqlens"].long(), st["new_lens"].long()
     used, total = _up(old, page), _up(old + new, page)
-    need = total - used
+    fits = total <= table.shape[1]                       # a request the table has no room for asks for nothing
+    need = (total - used) * fits
     last = torch.cumsum(need, 0)
-    served = ((need == 0) | (last <= st["n_free"].long())) & (total <= table.shape[1])
+    served = ((need == 0) | (last <= st["n_free"].long())) & fits
     first = last - need
     # new page k of the step is popped from the top of the stack
     col = torch.arange(table.shape[1], device=DEV)[None]
