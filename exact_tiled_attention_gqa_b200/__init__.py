@@ -12,12 +12,23 @@ Two calls, both thin wrappers over the C ABI in ``include/attn_gqa.h``:
 * ``decode_paged(q, k_pages, v_pages, block_table, seqlens)`` -- decode_mq over
   a paged cache: pools [n_pages,Hkv,page_size,D] and a block table [B,max_pages].
 
-Both return ``(out, lse)``: out bf16 shaped like q, lse fp32 (natural log).
+Around the cache, in the order a serving step that verifies drafted trees makes them:
+
+* ``page_plan`` / ``page_release`` -- block tables and slot maps from request
+  lengths, pages from and back to a free list, all on the device.
+* ``rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache)`` --
+  rotary positions (1 to 4 axes) of the new tokens, K and V to their cache slots.
+* ``decode_tree`` / ``decode_tree_paged`` -- decode_mq with the order among the
+  new tokens given by a tree mask (``pack_tree_mask``).
+* ``tree_commit`` -- the accepted path's rows move together, the lengths follow.
+
+The attention calls return ``(out, lse)``: out bf16 shaped like q, lse fp32 (natural log).
 PyTorch supplies device memory and the current stream; every step of the
 computation runs in the library's CUDA kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional
@@ -29,7 +40,8 @@ from ._native import AttnError
 
 __all__ = ["prefill", "prefill_workspace_size", "prefill_host", "decode", "decode_host", "decode_host_workspace_size", "decode_partial", "decode_merge", "decode_merge_peers", "kvp_signal",
            "kvp_wait", "decode_mq", "decode_paged", "decode_noalloc", "decode_kv8", "decode_kv8_paged", "prefill_host_scratch_size", "decode_workspace_size", "decode_mq_workspace_size",
-           "decode_kv8_workspace_size", "device_error", "AttnError", "library_path"]
+           "decode_kv8_workspace_size", "decode_tree", "decode_tree_paged", "decode_tree_workspace_size", "decode_tree_paged_workspace_size",
+           "pack_tree_mask", "page_plan", "page_release", "rope_append", "tree_commit", "device_error", "AttnError", "library_path"]
 
 
 def library_path() -> str:
@@ -542,6 +554,292 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                                                _ptr(lse), B, Hq, Hkv, Lmax, D, float(scale), _stream_handle(stream))
     _native.check(st, "attn_decode_noalloc")
     return out, lse
+
+
+def _allocate_on(stream, device: torch.device):
+    """Context in which a call's own results and workspace are allocated: they belong to the
+    stream that uses them, so memory another stream still works on is not handed out for them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, but the call's tensors are on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _c_int(name: str, x: int, low: int = 0) -> int:
+    x = int(x)
+    if not low <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{name}={x} must lie in [{low}, 2^31 - 1]")
+    return x
+
+
+def pack_tree_mask(allowed: torch.Tensor) -> torch.Tensor:
+    """The tree_mask of decode_tree from truth values: allowed [..., T, T] bool, allowed[..., i, j] = node i
+    sees node j  ->  int32 [..., T, (T + 31) / 32], bit j % 32 of word j / 32."""
+    if not isinstance(allowed, torch.Tensor) or allowed.dtype != torch.bool or allowed.dim() < 2 \
+            or allowed.shape[-1] != allowed.shape[-2]:
+        raise ValueError("allowed must be a bool tensor [..., T, T]")
+    T = allowed.shape[-1]
+    bits = torch.nn.functional.pad(allowed, (0, -T % 32)).unflatten(-1, (-1, 32)).long()
+    words = (bits << torch.arange(32, device=allowed.device)).sum(-1)
+    return torch.where(words >= 1 << 31, words - (1 << 32), words).int()
+
+
+def _check_tree(q, tree_mask, tree_lens, B: int, T: int) -> None:
+    if not isinstance(tree_mask, torch.Tensor) or tree_mask.dim() not in (2, 3):
+        raise ValueError("tree_mask must be a tensor [B,T,W] or [T,W]")
+    _check_tensor("tree_mask", tree_mask, torch.int32, tree_mask.dim())
+    want = (T, -(-T // 32)) if tree_mask.dim() == 2 else (B, T, -(-T // 32))
+    if tuple(tree_mask.shape) != want:
+        raise ValueError(f"tree_mask must have shape {want}, got {tuple(tree_mask.shape)}")
+    if tree_lens is not None:
+        _check_tensor("tree_lens", tree_lens, torch.int32, 1)
+        if tree_lens.shape[0] != B:
+            raise ValueError(f"tree_lens must have {B} entries")
+    _check_on(q.device, tree_mask=tree_mask, tree_lens=tree_lens)
+
+
+def decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, Lmax: int, D: int) -> int:
+    return int(_native.lib().attn_decode_tree_workspace_size(B, Hq, Hkv, T, Lmax, D))
+
+
+def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Tensor,
+                tree_mask: torch.Tensor, *, tree_lens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a tree of T drafted tokens per sequence.  q [B,Hq,T,D], caches [B,Hkv,Lmax,D] bf16, seqlens
+    int32 [B]; the last tree_lens[b] (int32 [B]; T when None) of a sequence's cached rows are its tree's nodes.
+    tree_mask int32 [B,T,W] or [T,W] (pack_tree_mask): node i sees every row before the tree and node j where bit
+    j is set.  Nodes at or past tree_lens[b], and nodes that see no row: out = 0, lse = -inf."""
+    _check_tensor("q", q, torch.bfloat16, 4)
+    _check_tensor("k_cache", k_cache, torch.bfloat16, 4)
+    _check_tensor("v_cache", v_cache, torch.bfloat16, 4)
+    _check_tensor("seqlens", seqlens, torch.int32, 1)
+    B, Hq, T, D = q.shape
+    Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
+    if k_cache.shape[0] != B or k_cache.shape[3] != D or v_cache.shape != k_cache.shape or seqlens.shape[0] != B:
+        raise ValueError("shape mismatch between q, the caches and seqlens")
+    _check_tree(q, tree_mask, tree_lens, B, T)
+    _check_on(q.device, k_cache=k_cache, v_cache=v_cache, seqlens=seqlens)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(q.device), _allocate_on(stream, q.device):
+        out = _result("out", out, torch.bfloat16, q.shape, q.device)
+        lse = _result("lse", lse, torch.float32, (B, Hq, T), q.device, want_lse)
+        workspace, ws_bytes = _workspace(workspace, decode_tree_workspace_size(B, Hq, Hkv, T, Lmax, D), q.device)
+        st = _native.lib().attn_decode_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(tree_mask),
+                                            int(tree_mask.dim() == 3), _ptr(tree_lens), _ptr(out), _ptr(lse), B, Hq,
+                                            Hkv, T, Lmax, D, float(scale), _ptr(workspace), ws_bytes,
+                                            _stream_handle(stream))
+    _native.check(st, "attn_decode_tree")
+    return out, lse
+
+
+def decode_tree_paged_workspace_size(B: int, Hq: int, Hkv: int, T: int, page_size: int, max_pages: int, D: int) -> int:
+    return int(_native.lib().attn_decode_tree_paged_workspace_size(B, Hq, Hkv, T, page_size, max_pages, D))
+
+
+def decode_tree_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                      seqlens: torch.Tensor, tree_mask: torch.Tensor, *, tree_lens: Optional[torch.Tensor] = None,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """decode_tree over a paged cache: pools [n_pages,Hkv,page_size,D], block_table int32 [B,max_pages]."""
+    _check_tensor("q", q, torch.bfloat16, 4)
+    _check_tensor("k_pages", k_pages, torch.bfloat16, 4)
+    _check_tensor("v_pages", v_pages, torch.bfloat16, 4)
+    _check_tensor("block_table", block_table, torch.int32, 2)
+    _check_tensor("seqlens", seqlens, torch.int32, 1)
+    B, Hq, T, D = q.shape
+    n_pages, Hkv, page_size = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
+    max_pages = block_table.shape[1]
+    if (k_pages.shape[3] != D or v_pages.shape != k_pages.shape or block_table.shape[0] != B
+            or seqlens.shape[0] != B):
+        raise ValueError("shape mismatch between q, the page pools, block_table and seqlens")
+    _check_tree(q, tree_mask, tree_lens, B, T)
+    _check_on(q.device, k_pages=k_pages, v_pages=v_pages, block_table=block_table, seqlens=seqlens)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(q.device), _allocate_on(stream, q.device):
+        out = _result("out", out, torch.bfloat16, q.shape, q.device)
+        lse = _result("lse", lse, torch.float32, (B, Hq, T), q.device, want_lse)
+        need = decode_tree_paged_workspace_size(B, Hq, Hkv, T, page_size, max_pages, D)
+        workspace, ws_bytes = _workspace(workspace, need, q.device)
+        st = _native.lib().attn_decode_tree_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                                                  _ptr(seqlens), _ptr(tree_mask), int(tree_mask.dim() == 3),
+                                                  _ptr(tree_lens), _ptr(out), _ptr(lse), B, Hq, Hkv, T, n_pages,
+                                                  page_size, max_pages, D, float(scale), _ptr(workspace), ws_bytes,
+                                                  _stream_handle(stream))
+    _native.check(st, "attn_decode_tree_paged")
+    return out, lse
+
+
+def page_plan(seqlens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+              n_free: torch.Tensor, *, L: int, page_size: int, n_pages: int, slots: Optional[torch.Tensor] = None,
+              out_seqlens: Optional[torch.Tensor] = None, out_n_free: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None):
+    """Pages and cache slots for new_lens[b] <= L new rows of every request (all int32 on one CUDA device).
+
+    seqlens, new_lens [B]; block_table [B,max_pages], written for the new pages; free_pages [capacity] with n_free
+    [1] valid entries, popped from the top, requests in order.  A request the pages do not reach for, or the table
+    has no room for, is refused: status 1, length as it was, slots -1.  Returns (slots [B,L], out_seqlens [B],
+    out_n_free [1], status [B]); out_seqlens may be seqlens and out_n_free n_free."""
+    for n, t, nd in (("seqlens", seqlens, 1), ("new_lens", new_lens, 1), ("block_table", block_table, 2),
+                     ("free_pages", free_pages, 1), ("n_free", n_free, 1)):
+        _check_tensor(n, t, torch.int32, nd)
+    B, L = seqlens.shape[0], _c_int("L", L)
+    if new_lens.shape[0] != B or block_table.shape[0] != B or n_free.shape[0] != 1:
+        raise ValueError("shape mismatch between seqlens, new_lens, block_table and n_free")
+    dev = seqlens.device
+    _check_on(dev, "seqlens", new_lens=new_lens, block_table=block_table, free_pages=free_pages, n_free=n_free)
+    with torch.cuda.device(dev), _allocate_on(stream, dev):
+        slots = _result("slots", slots, torch.int32, (B, L), dev)
+        out_seqlens = _result("out_seqlens", out_seqlens, torch.int32, (B,), dev)
+        out_n_free = _result("out_n_free", out_n_free, torch.int32, (1,), dev)
+        status = _result("status", status, torch.int32, (B,), dev)
+        st = _native.lib().attn_page_plan(_ptr(seqlens), _ptr(new_lens), _ptr(block_table), _ptr(free_pages),
+                                          _ptr(n_free), _ptr(slots), _ptr(out_seqlens), _ptr(out_n_free),
+                                          _ptr(status), B, L, _c_int("page_size", page_size), block_table.shape[1],
+                                          free_pages.shape[0], _c_int("n_pages", n_pages), _stream_handle(stream))
+    _native.check(st, "attn_page_plan")
+    return slots, out_seqlens, out_n_free, status
+
+
+def page_release(seqlens: torch.Tensor, keep_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                 n_free: torch.Tensor, *, page_size: int, n_pages: int, out_n_free: Optional[torch.Tensor] = None,
+                 stream=None):
+    """The pages past each request's first keep_lens[b] of seqlens[b] rows go back on the stack free_pages (written
+    from n_free on).  All int32 as in page_plan.  Returns out_n_free [1], which may be n_free."""
+    for n, t, nd in (("seqlens", seqlens, 1), ("keep_lens", keep_lens, 1), ("block_table", block_table, 2),
+                     ("free_pages", free_pages, 1), ("n_free", n_free, 1)):
+        _check_tensor(n, t, torch.int32, nd)
+    B = seqlens.shape[0]
+    if keep_lens.shape[0] != B or block_table.shape[0] != B or n_free.shape[0] != 1:
+        raise ValueError("shape mismatch between seqlens, keep_lens, block_table and n_free")
+    dev = seqlens.device
+    _check_on(dev, "seqlens", keep_lens=keep_lens, block_table=block_table, free_pages=free_pages, n_free=n_free)
+    with torch.cuda.device(dev), _allocate_on(stream, dev):
+        out_n_free = _result("out_n_free", out_n_free, torch.int32, (1,), dev)
+        st = _native.lib().attn_page_release(_ptr(seqlens), _ptr(keep_lens), _ptr(block_table), _ptr(free_pages),
+                                             _ptr(n_free), _ptr(out_n_free), B, _c_int("page_size", page_size),
+                                             block_table.shape[1], free_pages.shape[0], _c_int("n_pages", n_pages),
+                                             _stream_handle(stream))
+    _native.check(st, "attn_page_release")
+    return out_n_free
+
+
+def _token_stride(name: str, t: torch.Tensor) -> int:
+    """Elements from one token of t [B,L,H,D] to the next, heads dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-d bf16 CUDA tensor [B,L,H,D]")
+    B, L, H, D = t.shape
+    dense = H * D
+    if t.numel() == 0:
+        return dense
+    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    step = t.stride(1) if L > 1 else t.stride(0) if B > 1 else dense
+    if B > 1 and L > 1 and t.stride(0) != L * step:
+        raise ValueError(f"the tokens of {name} must lie one stride apart (as in a part of one projection's output)")
+    return step
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, sections=None,
+                axis_order: str = "blocks", pairs: str = "half", k_scale: Optional[torch.Tensor] = None,
+                v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """Turn q and k by their rotary positions and write k and v to the cache.
+
+    q [B,L,Hq,D], k and v [B,L,Hkv,D] bf16 (parts of one projection's output may be passed as they are);
+    positions int32 [n_axes,B,L] (or [B,L] for one axis); inv_freq fp32 [rot / 2]; slots int32 [B,L], as page_plan
+    writes them (below 0: not stored; no two tokens may share one).  Caches [n,Hkv,rows,D]: bf16, or with
+    k_scale / v_scale torch.float8_e4m3fn (scales fp32 [Hkv], read) or torch.int8 (fp16 [n,Hkv,rows,D/32], written).
+    sections: pairs per axis (default: all on one axis); axis_order "blocks" or "cycle" (axes taken in turn);
+    pairs "half" (i, i + rot / 2) or "adjacent" (2i, 2i + 1).  Returns the turned q as [B,Hq,L,D] bf16."""
+    steps = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v))]
+    B, L, Hq, D = q.shape
+    Hkv = k.shape[2]
+    if k.shape != (B, L, Hkv, D) or v.shape != k.shape:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
+    if isinstance(positions, torch.Tensor) and positions.dim() == 2:
+        positions = positions.unsqueeze(0)
+    _check_tensor("positions", positions, torch.int32, 3)
+    _check_tensor("inv_freq", inv_freq, torch.float32, 1)
+    _check_tensor("slots", slots, torch.int32, 2)
+    n_axes, rot = positions.shape[0], 2 * inv_freq.shape[0]
+    if positions.shape[1:] != (B, L) or slots.shape != (B, L):
+        raise ValueError("positions must be [n_axes,B,L] and slots [B,L]")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.int8):
+        raise TypeError("k_cache must be a bfloat16, float8_e4m3fn or int8 tensor")
+    _check_tensor("k_cache", k_cache, k_cache.dtype, 4)
+    _check_tensor("v_cache", v_cache, k_cache.dtype, 4)
+    n_outer, rows = k_cache.shape[0], k_cache.shape[2]
+    if k_cache.shape != (n_outer, Hkv, rows, D) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"the caches must be [n,{Hkv},rows,{D}]")
+    fmt, want = 0, None
+    if k_cache.dtype == torch.float8_e4m3fn:
+        fmt, sdt, want = _native.ATTN_KV_E4M3, torch.float32, (Hkv,)
+    elif k_cache.dtype == torch.int8:
+        fmt, sdt, want = _native.ATTN_KV_Q8_0, torch.float16, (n_outer, Hkv, rows, D // 32)
+    for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if (t is None) != (want is None):
+            raise ValueError(f"{n} goes with an 8-bit cache, and only with one")
+        if want is not None:
+            _check_tensor(n, t, sdt, len(want))
+            if tuple(t.shape) != want:
+                raise ValueError(f"{n} must have shape {want}")
+    _check_on(q.device, k=k, v=v, positions=positions, inv_freq=inv_freq, slots=slots, k_cache=k_cache,
+              v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    sections = [rot // 2] if sections is None else [_c_int("sections", x) for x in sections]
+    if len(sections) != n_axes:
+        raise ValueError(f"{n_axes} position axes need as many sections, got {len(sections)}")
+    if axis_order not in ("blocks", "cycle") or pairs not in ("half", "adjacent"):
+        raise ValueError("axis_order must be 'blocks' or 'cycle', pairs 'half' or 'adjacent'")
+    with torch.cuda.device(q.device), _allocate_on(stream, q.device):
+        out = _result("out", out, torch.bfloat16, (B, Hq, L, D), q.device)
+        st = _native.lib().attn_rope_append(_ptr(q), _ptr(k), _ptr(v), *steps, _ptr(positions), _ptr(inv_freq),
+                                            _ptr(slots), _ptr(out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                            _ptr(v_scale), fmt, B, L, Hq, Hkv, D, rot, n_outer, rows, n_axes,
+                                            (ctypes.c_int * max(1, n_axes))(*sections), int(axis_order == "cycle"),
+                                            int(pairs == "adjacent"), _stream_handle(stream))
+    _native.check(st, "attn_rope_append")
+    return out
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Tensor, accept: torch.Tensor,
+                n_accept: torch.Tensor, *, T: int, block_table: Optional[torch.Tensor] = None,
+                tree_lens: Optional[torch.Tensor] = None, out_seqlens: Optional[torch.Tensor] = None, stream=None):
+    """Move the accepted path's K and V rows together after decode_tree.  Caches bf16 [B,Hkv,Lmax,D], or pools
+    [n_pages,Hkv,page_size,D] with block_table int32 [B,max_pages]; seqlens int32 [B] with the tree's rows;
+    accept int32 [B,A] the path's nodes, increasing, the first n_accept[b] of them taken.  T, tree_lens as in
+    decode_tree.  Returns out_seqlens int32 [B] (may be seqlens): the rows before the tree plus n_accept."""
+    _check_tensor("k_cache", k_cache, torch.bfloat16, 4)
+    _check_tensor("v_cache", v_cache, torch.bfloat16, 4)
+    for n, t, nd in (("seqlens", seqlens, 1), ("accept", accept, 2), ("n_accept", n_accept, 1)):
+        _check_tensor(n, t, torch.int32, nd)
+    B = seqlens.shape[0]
+    if v_cache.shape != k_cache.shape or accept.shape[0] != B or n_accept.shape[0] != B:
+        raise ValueError("shape mismatch between the caches, seqlens, accept and n_accept")
+    if block_table is not None:
+        _check_tensor("block_table", block_table, torch.int32, 2)
+    if tree_lens is not None:
+        _check_tensor("tree_lens", tree_lens, torch.int32, 1)
+    if (k_cache.shape[0] != B if block_table is None else block_table.shape[0] != B) \
+            or (tree_lens is not None and tree_lens.shape[0] != B):
+        raise ValueError("shape mismatch between seqlens, the caches, block_table and tree_lens")
+    dev = k_cache.device
+    _check_on(dev, "k_cache", v_cache=v_cache, seqlens=seqlens, accept=accept, n_accept=n_accept,
+              block_table=block_table, tree_lens=tree_lens)
+    n_outer, Hkv, rows, D = k_cache.shape
+    with torch.cuda.device(dev), _allocate_on(stream, dev):
+        out_seqlens = _result("out_seqlens", out_seqlens, torch.int32, (B,), dev)
+        st = _native.lib().attn_tree_commit(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seqlens),
+                                            _ptr(tree_lens), _ptr(accept), _ptr(n_accept), _ptr(out_seqlens), B, Hkv,
+                                            _c_int("T", T), accept.shape[1], D, n_outer, rows,
+                                            0 if block_table is None else block_table.shape[1],
+                                            _stream_handle(stream))
+    _native.check(st, "attn_tree_commit")
+    return out_seqlens
 
 
 def device_error(reset: bool = True) -> int:

@@ -28,12 +28,13 @@ ATTN_DEVERR_SEQLEN = 0x2
 ATTN_DEVERR_PAGE = 0x4
 ATTN_DEVERR_SCHED = 0x8
 ATTN_DEVERR_BOUNDS = 0x10
+ATTN_DEVERR_INDEX = 0x20
 ATTN_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20
 ATTN_KV_E4M3 = 1
 ATTN_KV_Q8_0 = 2
 
 # name -> (restype, argtypes): every symbol the header declares
-_vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_vp, _i32, _f32, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 SIGNATURES = {
     "attn_prefill": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp]),
     "attn_prefill_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
@@ -64,6 +65,17 @@ SIGNATURES = {
     "attn_decode_kv8_paged_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "attn_decode_kv8_paged": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                      _i32, _i32, _i32, _f32, _vp, _sz, _vp]),
+    "attn_decode_tree_workspace_size": (_sz, [_i32] * 6),
+    "attn_decode_tree": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                                _vp, _sz, _vp]),
+    "attn_decode_tree_paged_workspace_size": (_sz, [_i32] * 7),
+    "attn_decode_tree_paged": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                      _i32, _i32, _i32, _f32, _vp, _sz, _vp]),
+    "attn_page_plan": (_i32, [_vp] * 9 + [_i32] * 6 + [_vp]),
+    "attn_page_release": (_i32, [_vp] * 6 + [_i32] * 5 + [_vp]),
+    "attn_rope_append": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                                _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), _i32, _i32, _vp]),
+    "attn_tree_commit": (_i32, [_vp] * 8 + [_i32] * 8 + [_vp]),
     "attn_selftest_kv8_convert": (_i32, [_vp, _vp, _i32, _i32, _vp]),
     "attn_selftest_wait": (_i32, [ctypes.c_ulonglong, _vp, _vp]),
     "attn_prefill_sched_busy": (_i32, [ctypes.POINTER(_i32)]),

@@ -20,6 +20,8 @@
 #include "decode_sm100.cuh"
 #include "decode_tc_sm100.cuh"
 #include "prefill_sm100.cuh"
+#include "serving_sm100.cuh"
+#include "tree_sm100.cuh"
 
 namespace attn {
 namespace {
@@ -187,13 +189,13 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned b
 // The split combine: one warp per row (four rows per CTA) when rows have few
 // splits, four warps per row when they have more than 16 (their reads then take
 // four times fewer dependent rounds).
-template <int D, bool F32>
+template <int D, bool F32, bool NANLSE = false>
 int launch_combine(const DecodeParams& prm, void* out, float* lse, int rows, cudaStream_t stream) {
     const cudaError_t e =
         (prm.n_splits > 16)
-            ? launch_dependent(attn_decode_combine_kernel<D, F32, 4>, static_cast<unsigned>(rows), 128u, stream, prm,
+            ? launch_dependent(attn_decode_combine_kernel<D, F32, 4, NANLSE>, static_cast<unsigned>(rows), 128u, stream, prm,
                                out, lse)
-            : launch_dependent(attn_decode_combine_kernel<D, F32, 1>, static_cast<unsigned>((rows + 3) / 4), 128u,
+            : launch_dependent(attn_decode_combine_kernel<D, F32, 1, NANLSE>, static_cast<unsigned>((rows + 3) / 4), 128u,
                                stream, prm, out, lse);
     if (e != cudaSuccess)
         return fail(ATTN_ERR_CUDA, "attn_decode_combine_kernel launch failed: %s", cudaGetErrorString(e));
@@ -1367,3 +1369,5 @@ extern "C" int attn_selftest_kv8_convert(const uint16_t* codes, uint32_t* out, i
     const int st = check_launch("kv8_convert_selftest_kernel");
     return st == ATTN_OK ? ok() : st;
 }
+
+#include "serving_api.cuh"

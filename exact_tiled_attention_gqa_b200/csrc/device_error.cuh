@@ -12,6 +12,7 @@ constexpr unsigned int kDevErrSeqlen = 0x2u;    // ATTN_DEVERR_SEQLEN
 constexpr unsigned int kDevErrPage = 0x4u;      // ATTN_DEVERR_PAGE
 constexpr unsigned int kDevErrSched = 0x8u;     // ATTN_DEVERR_SCHED
 constexpr unsigned int kDevErrBounds = 0x10u;   // ATTN_DEVERR_BOUNDS (builds with ATTN_DEBUG_BOUNDS)
+constexpr unsigned int kDevErrIndex = 0x20u;    // ATTN_DEVERR_INDEX
 
 __device__ unsigned int g_attn_err;
 

@@ -507,6 +507,183 @@ int attn_decode_kv8_paged(const void* q, const void* k_pages, const void* v_page
                           int max_pages, int D, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * attn_decode_tree_workspace_size / attn_decode_tree -- attention of a tree of
+ * drafted tokens over a KV cache: the verify step of speculative decoding when
+ * the draft is a tree.  attn_decode_mq with the order among the new tokens
+ * given by a mask instead of by their positions.
+ *
+ * Sequence b has n = seqlens[b] cached rows; the last n_b = tree_lens[b] (T
+ * when tree_lens is NULL) are the nodes of its tree.  With c = n - n_b, node
+ * i < n_b sees the rows 0 .. c - 1 and, of the tree, row c + j for every j < n_b
+ * whose bit is set: bit j % 32 of tree_mask[b][i][j / 32].  A node that should
+ * see itself has its own bit set.  Nodes i >= n_b, and nodes that see no row,
+ * get O = 0 and LSE = -inf.  When n < n_b, the rows c + j < 0 do not exist.
+ * Rows a node does not see (K, V, NaN included) have no effect on it.
+ *
+ *   q          [B, Hq, T, D]        bf16, read
+ *   k_cache, v_cache                [B, Hkv, Lmax, D] bf16, read (rows >= seqlens[b] unused)
+ *   seqlens    [B]                  int32, as attn_decode
+ *   tree_mask  [B, T, W] or [T, W]  uint32, read; W = (T + 31) / 32; [T, W] (one mask for
+ *                                   every sequence) when mask_per_seq == 0
+ *   tree_lens  [B] or NULL          int32 in device memory, each in [0, T]; a value outside
+ *                                   is clamped and flags ATTN_DEVERR_INDEX
+ *   out        [B, Hq, T, D]        bf16, written
+ *   lse        [B, Hq, T]           fp32, written; may be NULL
+ *   workspace  attn_decode_tree_workspace_size(...) bytes, 256-byte aligned, as attn_decode
+ *   D: 64, 128 or 256.  T: 1 .. 1024.  Any Hq / Hkv.
+ *
+ * Errors: as attn_decode, plus ATTN_ERR_INVALID_ARG for T < 1 or a null
+ * tree_mask and ATTN_ERR_UNSUPPORTED for T > 1024.
+ */
+size_t attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int T, int Lmax, int D);
+int attn_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* seqlens,
+                     const uint32_t* tree_mask, int mask_per_seq, const int32_t* tree_lens, void* out, float* lse,
+                     int B, int Hq, int Hkv, int T, int Lmax, int D, float scale, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * attn_decode_tree_paged_workspace_size / attn_decode_tree_paged --
+ * attn_decode_tree over the paged cache of attn_decode_paged (pools
+ * [n_pages, Hkv, page_size, D], block_table [B, max_pages], page_size a
+ * positive multiple of 64).  Other arguments and errors as attn_decode_tree
+ * and attn_decode_paged.
+ */
+size_t attn_decode_tree_paged_workspace_size(int B, int Hq, int Hkv, int T, int page_size, int max_pages, int D);
+int attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                           const int32_t* seqlens, const uint32_t* tree_mask, int mask_per_seq,
+                           const int32_t* tree_lens, void* out, float* lse, int B, int Hq, int Hkv, int T, int n_pages,
+                           int page_size, int max_pages, int D, float scale, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * attn_page_plan -- the pages and cache slots of a step's new rows, from the
+ * requests' lengths: block tables and slot maps without the host.
+ *
+ * Request b has seqlens[b] rows and gets new_lens[b] more.  It holds
+ * ceil(seqlens[b] / page_size) pages, in block_table[b]; the new ones it needs
+ * are popped from the top of the stack free_pages[0 .. n_free), requests in
+ * order.  A request whose table row has no room (more than max_pages pages) is
+ * refused and asks for nothing; one that needs pages when the needs up to and
+ * with its own pass n_free is refused too, and its need still counts for those
+ * after it (a request that needs no page is always served).
+ *
+ *   seqlens     [B]             int32, read
+ *   new_lens    [B]             int32, read; each in [0, L]
+ *   block_table [B, max_pages]  int32; the entries of new pages are written, others untouched
+ *   free_pages  [capacity]      int32, read: the popped entries stay where they are, above
+ *                               the new top
+ *   n_free      [1]             int32, read; in [0, capacity]
+ *   slots       [B, L]          int32, written: page * page_size + row % page_size of new
+ *                               row j < new_lens[b] of a served request, -1 elsewhere
+ *   out_seqlens [B]             int32, written: the length with the new rows (refused: as it
+ *                               was).  May be seqlens.
+ *   out_n_free  [1]             int32, written: pages left.  May be n_free.
+ *   status      [B]             int32, written: 0 served, 1 refused
+ *
+ * Other overlaps of the arrays are not allowed.  A length below 0, a new length
+ * above L or a length above max_pages * page_size refuses the request and flags
+ * ATTN_DEVERR_SEQLEN; an n_free outside [0, capacity] is clamped and flags
+ * ATTN_DEVERR_PAGE, as does a page outside [0, n_pages), whose slots are -1.
+ * Limits: n_pages * page_size and max_pages * page_size below 2^31, B * max_pages
+ * and capacity below 2^30.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
+ * ATTN_ERR_CUDA.
+ */
+int attn_page_plan(const int32_t* seqlens, const int32_t* new_lens, int32_t* block_table, const int32_t* free_pages,
+                   const int32_t* n_free, int32_t* slots, int32_t* out_seqlens, int32_t* out_n_free, int32_t* status,
+                   int B, int L, int page_size, int max_pages, int capacity, int n_pages, void* stream);
+
+/*
+ * attn_page_release -- the inverse: request b keeps its first keep_lens[b] of
+ * seqlens[b] rows (0: it has ended), and the pages past them go back on the
+ * stack, requests in order and each one's pages in order.
+ *
+ *   seqlens, keep_lens [B]  int32, read; 0 <= keep_lens[b] <= seqlens[b]; a pair that is
+ *                           not releases nothing and flags ATTN_DEVERR_SEQLEN
+ *   block_table             read (entries are left as they are)
+ *   free_pages [capacity]   int32, written from n_free on
+ *   n_free, out_n_free [1]  int32, read / written; may be the same
+ *
+ * Pages that would pass the stack's capacity are dropped and flag
+ * ATTN_DEVERR_PAGE; an entry outside [0, n_pages) flags it too (and is put on
+ * the stack as it is).  Limits and errors as attn_page_plan.
+ */
+int attn_page_release(const int32_t* seqlens, const int32_t* keep_lens, const int32_t* block_table,
+                      int32_t* free_pages, const int32_t* n_free, int32_t* out_n_free, int B, int page_size,
+                      int max_pages, int capacity, int n_pages, void* stream);
+
+/*
+ * attn_rope_append -- rotary positions of a step's new tokens, and their K and
+ * V written to the cache: what comes between a layer's projection and the
+ * decode calls.
+ *
+ * The first `rot` elements of a q or k head are rot / 2 pairs, elements i and
+ * i + rot / 2 (adjacent == 0) or 2i and 2i + 1 (adjacent != 0).  Pair i = (a, b)
+ * becomes (a cos t - b sin t, b cos t + a sin t) with
+ * t = positions[axis(i)][token] * inv_freq[i].  The axes (1 to 4: time, height,
+ * width, ..) have sections[0 .. n_axes) pairs each, rot / 2 in all:
+ *   axis_cycle == 0: in blocks, the first sections[0] pairs axis 0, and so on;
+ *   axis_cycle != 0: in turn; axis a > 0 has the pairs a, a + n_axes, ..., the
+ *                    first sections[a] of them, and axis 0 all others.
+ * V and the elements from rot on are not turned.  Angles are exact to about
+ * 2e-7 radians at any position; arithmetic is fp32, rounded once.
+ *
+ *   q [B, L, Hq, D], k, v [B, L, Hkv, D]  bf16, read; a token's heads are dense, tokens lie
+ *                 q_stride, k_stride, v_stride elements apart (multiples of 8), so the three
+ *                 may be parts of one projection's output
+ *   positions     [n_axes, B, L]     int32, read (any sign)
+ *   inv_freq      [rot / 2]          fp32, read
+ *   slots         [B, L]             int32, read: row slot % page_size of slab slot / page_size
+ *                 takes the token's K and V.  Below 0: nowhere.  At or above
+ *                 n_outer * page_size: nowhere, and ATTN_DEVERR_PAGE is flagged.  Two tokens
+ *                 of one call must not have the same slot.
+ *   q_out         [B, Hq, L, D]      bf16, written for every token (the q of the decode calls);
+ *                 must not overlap q, k or v
+ *   k_cache, v_cache  [n_outer, Hkv, page_size, D], written: a pool of pages, or contiguous
+ *                 caches (n_outer = B, page_size = Lmax).  kv_format 0: bf16.
+ *                 ATTN_KV_E4M3: codes of x / scale of the head, to nearest even, saturating
+ *                 at +-448; ATTN_KV_Q8_0: per 32 elements the scale fp16(max |x| / 127)
+ *                 (at most 65504) and the codes x / scale to nearest even, in [-127, 127].
+ *   k_scale, v_scale  ATTN_KV_E4M3: fp32 [Hkv], read.  ATTN_KV_Q8_0: fp16
+ *                 [n_outer, Hkv, page_size, D / 32], written.  kv_format 0: not used.
+ *   D: 64, 128 or 256 (8-bit caches: 64 and 128).  rot: a multiple of 16, 0 .. D.
+ *   sections is read during the call, in host memory.
+ *
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.  B * L == 0
+ * returns ATTN_OK.
+ */
+int attn_rope_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                     long long v_stride, const int32_t* positions, const float* inv_freq, const int32_t* slots,
+                     void* q_out, void* k_cache, void* v_cache, void* k_scale, void* v_scale, int kv_format, int B,
+                     int L, int Hq, int Hkv, int D, int rot, int n_outer, int page_size, int n_axes,
+                     const int* sections, int axis_cycle, int adjacent, void* stream);
+
+/*
+ * attn_tree_commit -- after verification: the rows of the accepted path move
+ * together behind the context, and the lengths follow.
+ *
+ * With n_b and c as in attn_decode_tree, cache row c + j of K and V becomes row
+ * c + accept[b][j] for j < n_accept[b], and out_seqlens[b] = c + n_accept[b].
+ * accept[b] increases (nodes are numbered parents first) and lies in [0, n_b).
+ *
+ *   k_cache, v_cache  [n_outer, Hkv, page_size, D] bf16, read and written: a pool of pages
+ *                 with block_table [B, max_pages], or contiguous caches (block_table NULL,
+ *                 n_outer >= B, page_size = Lmax, max_pages unused).  Two sequences must not
+ *                 share the pages of their tree rows.
+ *   seqlens, tree_lens (or NULL: T)  as attn_decode_tree
+ *   accept      [B, A]   int32, read
+ *   n_accept    [B]      int32, read; in [0, min(A, n_b)]
+ *   out_seqlens [B]      int32, written; may be seqlens
+ *
+ * A length or a path that cannot be moves nothing, leaves the length as it is
+ * and flags ATTN_DEVERR_SEQLEN or ATTN_DEVERR_INDEX; rows in a page outside the
+ * pool are left out and flag ATTN_DEVERR_PAGE.  D: 64, 128 or 256.  T: 1 .. 1024.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ */
+int attn_tree_commit(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seqlens,
+                     const int32_t* tree_lens, const int32_t* accept, const int32_t* n_accept, int32_t* out_seqlens,
+                     int B, int Hkv, int T, int A, int D, int n_outer, int page_size, int max_pages, void* stream);
+
+/*
  * attn_selftest_kv8_convert -- diagnostic: out[i] = the f16x2 (two f16 bit
  * patterns, code byte 0 in bits 0-15) that attn_decode_kv8 feeds its MMAs for
  * the two 8-bit codes in codes[i] (byte 0 in bits 0-7), for kv_format
@@ -565,13 +742,17 @@ const char* attn_last_error(void);
  * sets a bit here and the kernel returns early.
  */
 #define ATTN_DEVERR_TIMEOUT 0x1u  /* a pipeline wait gave up after ~2 s */
-#define ATTN_DEVERR_SEQLEN  0x2u  /* a seqlens value was outside [0, Lmax] */
-#define ATTN_DEVERR_PAGE    0x4u  /* a block_table entry was outside [0, n_pages) */
+#define ATTN_DEVERR_SEQLEN  0x2u  /* a seqlens value was outside [0, Lmax], or a length that cannot be
+                                     (attn_page_plan, attn_page_release, attn_tree_commit) */
+#define ATTN_DEVERR_PAGE    0x4u  /* a block_table entry was outside [0, n_pages), an n_free outside
+                                     [0, capacity], or a slot outside the cache */
 #define ATTN_DEVERR_SCHED   0x8u  /* a prefill launch shared its scheduling counters with another
                                      launch running at the same time (see attn_prefill) */
 #define ATTN_DEVERR_BOUNDS  0x10u /* only in the library built with -DATTN_DEBUG_BOUNDS=1: a work-unit
                                      mapping, ring position, TMA coordinate or output index fell
                                      outside its tensor (a checking build for tests) */
+#define ATTN_DEVERR_INDEX   0x20u /* a tree_lens value, or an accepted path, that cannot be
+                                     (attn_decode_tree, attn_tree_commit) */
 
 /*
  * attn_device_error -- synchronise the current device, copy its error word
