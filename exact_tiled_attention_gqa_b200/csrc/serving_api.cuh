@@ -180,6 +180,28 @@ int check_plan(const PlanParams& p) {
         return fail(ATTN_ERR_UNSUPPORTED, "block table or page stack too large");
     return ATTN_OK;
 }
+// Slots up to this many are written by attn_page_plan_kernel itself.
+constexpr long long kPlanSlots = 32768;
+// Table entries up to this many (at most, by the sizes) are copied by one CTA, more by a cluster.
+constexpr long long kPlanEntries = 4096;
+
+int launch_plan(void (*kernel)(const PlanParams), long long entries, cudaStream_t s, const PlanParams& p, const char* what) {
+    cudaLaunchAttribute attr[1];
+    const unsigned n = entries > kPlanEntries ? kPlanCluster : 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+    return check_launch(what);
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -194,12 +216,16 @@ extern "C" int attn_page_plan(const int32_t* seqlens, const int32_t* new_lens, i
     if (B > 0 && (!out_seqlens || !status || (!slots && L > 0)))
         return fail(ATTN_ERR_INVALID_ARG, "null slots, out_seqlens or status");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    attn_page_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
-    if ((st = check_launch("attn_page_plan_kernel")) != ATTN_OK) return st;
     const long long n = static_cast<long long>(B) * L;
-    if (n > 0) {
-        const unsigned grid = static_cast<unsigned>(std::min<long long>((n + 255) / 256, 148 * 8));
-        const cudaError_t e = launch_dependent(attn_page_slots_kernel, grid, 256u, s, p);
+    const bool slots_too = n <= kPlanSlots;
+    const long long entries = static_cast<long long>(B) * std::min(max_pages, L / page_size + 1);
+    if ((st = slots_too ? launch_plan(attn_page_plan_kernel<true>, entries, s, p, "attn_page_plan_kernel")
+                        : launch_plan(attn_page_plan_kernel<false>, entries, s, p, "attn_page_plan_kernel")) != ATTN_OK)
+        return st;
+    if (!slots_too) {
+        const long long units = static_cast<long long>(B) * ((L + static_cast<long long>(kSlotRun) - 1) / kSlotRun);
+        const unsigned grid = static_cast<unsigned>(std::min<long long>(units, 148 * 64));
+        const cudaError_t e = launch_dependent(attn_page_slots_kernel, grid, static_cast<unsigned>(kSlotThreads), s, p);
         if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "attn_page_slots_kernel launch failed: %s", cudaGetErrorString(e));
         if ((st = check_launch("attn_page_slots_kernel")) != ATTN_OK) return st;
     }
@@ -213,8 +239,8 @@ extern "C" int attn_page_release(const int32_t* seqlens, const int32_t* keep_len
                     out_n_free, nullptr, B, 0, page_size, max_pages, capacity, n_pages};
     int st = check_plan(p);
     if (st != ATTN_OK) return st;
-    attn_page_release_kernel<<<1, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    st = check_launch("attn_page_release_kernel");
+    st = launch_plan(attn_page_release_kernel, static_cast<long long>(B) * max_pages, static_cast<cudaStream_t>(stream), p,
+                     "attn_page_release_kernel");
     return st == ATTN_OK ? ok() : st;
 }
 
@@ -222,14 +248,22 @@ extern "C" int attn_page_release(const int32_t* seqlens, const int32_t* keep_len
 
 namespace attn {
 namespace {
+// Four tokens a CTA once that leaves four CTAs to each of 148 SMs, else one.
+constexpr long long kRopeManyTokens = 148LL * 4 * kRopeTokens;
+
+template <int D, int FMT, int TOK>
+int launch_rope_tokens(const RopeParams& p, bool adjacent, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.B) * p.L + TOK - 1) / TOK);
+    if (adjacent)
+        attn_rope_append_kernel<D, FMT, true, TOK><<<grid, kRopeThreads, 0, s>>>(p);
+    else
+        attn_rope_append_kernel<D, FMT, false, TOK><<<grid, kRopeThreads, 0, s>>>(p);
+    return check_launch("attn_rope_append_kernel");
+}
 template <int D, int FMT>
 int launch_rope(const RopeParams& p, bool adjacent, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(p.B * p.L);
-    if (adjacent)
-        attn_rope_append_kernel<D, FMT, true><<<grid, kRopeThreads, 0, s>>>(p);
-    else
-        attn_rope_append_kernel<D, FMT, false><<<grid, kRopeThreads, 0, s>>>(p);
-    return check_launch("attn_rope_append_kernel");
+    return static_cast<long long>(p.B) * p.L >= kRopeManyTokens ? launch_rope_tokens<D, FMT, kRopeTokens>(p, adjacent, s)
+                                                                : launch_rope_tokens<D, FMT, 1>(p, adjacent, s);
 }
 template <int D>
 int launch_rope_fmt(const RopeParams& p, int fmt, bool adjacent, cudaStream_t s) {

@@ -21,6 +21,7 @@ namespace attn {
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCluster = 8;
 
 struct PlanParams {
     const int* seqlens;      // [B] rows each request holds
@@ -74,19 +75,69 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
     return inc - x + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// One CTA: the scan, the table's new entries and the lengths, requests in chunks of
-// the block.  Every input of a chunk is read before its outputs are written, so
-// out_seqlens may be seqlens and out_n_free n_free.
+// All CTAs of the launch (one cluster, or a single CTA) have come here.
+__device__ __forceinline__ void plan_sync() {
+    if (gridDim.x == 1) {
+        __syncthreads();
+    } else {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+}
+
+// One warp's share of a copy of runs: entries lo[i] .. hi[i] - 1 of request i for
+// i = w, w + step, ... < n; load(i, c) gives a value, store(i, c, value) puts it.
+// kPlanInFlight rows of 32 entries are loaded before the first of them is stored:
+// one at a time, each request of a warp costs a round trip to memory (512 requests
+// of 64 pages: 15.6 us on one CTA one at a time).
+constexpr int kPlanInFlight = 8;
+
+template <typename Load, typename Store>
+__device__ __forceinline__ void plan_copy_runs(const int* lo, const int* hi, int w, int step, int n, Load load,
+                                               Store store) {
+    const int lane = threadIdx.x & 31;
+    int i = w, c = w < n ? lo[w] : 0;
+    while (i < n) {
+        int value[kPlanInFlight], at_i[kPlanInFlight], at_c[kPlanInFlight];
+#pragma unroll
+        for (int u = 0; u < kPlanInFlight; ++u) {
+            while (i < n && c >= hi[i]) {
+                i += step;
+                if (i < n) c = lo[i];
+            }
+            at_i[u] = -1;
+            if (i < n) {
+                if (c + lane < hi[i]) {
+                    at_i[u] = i;
+                    at_c[u] = c + lane;
+                    value[u] = load(i, c + lane);
+                }
+                c += 32;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kPlanInFlight; ++u)
+            if (at_i[u] >= 0) store(at_i[u], at_c[u], value[u]);
+    }
+}
+
+// The scan, the table's new entries, the lengths and, with SLOTS, the slots; requests in
+// chunks of the block.  One CTA, or a cluster of kPlanCluster CTAs that all scan (the
+// lengths are few) and share the copies.  Every CTA has read a chunk's lengths, and n_free,
+// before any writes that chunk's outputs, so out_seqlens may be seqlens and out_n_free n_free.
+template <bool SLOTS>
 __global__ void __launch_bounds__(kPlanThreads) attn_page_plan_kernel(const PlanParams p) {
     grid_dep_release();
     __shared__ long long warp_sums[32];
+    __shared__ int s_have[kPlanThreads], s_rows[kPlanThreads];      // rows held, rows given
     __shared__ int s_used[kPlanThreads], s_total[kPlanThreads], s_first[kPlanThreads];
     const int n_free = plan_n_free(p);
+    const int rank = blockIdx.x, n_cta = gridDim.x;
     long long before = 0;          // pages asked for by earlier chunks
     long long taken = 0;           // pages given
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
+        const int n = min(kPlanThreads, p.B - b0);
         int used = 0, total = 0, have = 0, want = 0;
         bool fits = false;
         if (b < p.B) {
@@ -106,55 +157,93 @@ __global__ void __launch_bounds__(kPlanThreads) attn_page_plan_kernel(const Plan
         long long asked;
         const long long first = before + block_scan(need, warp_sums, asked);
         const bool served = fits && (need == 0 || first + need <= n_free);
+        // requests are refused from the first one the pages do not reach for, so the pages given
+        // are the served needs' sum
         long long given;
-        block_scan(served ? need : 0, warp_sums, given);
+        if (before + asked <= n_free)
+            given = asked;
+        else
+            block_scan(served ? need : 0, warp_sums, given);
+        s_have[threadIdx.x] = have;
+        s_rows[threadIdx.x] = served ? want : 0;
         s_used[threadIdx.x] = used;
         s_total[threadIdx.x] = served ? total : used;
         s_first[threadIdx.x] = served ? static_cast<int>(first) : 0;
-        if (b < p.B) {
+        plan_sync();
+        if (rank == 0 && b < p.B) {
             p.out_seqlens[b] = served ? have + want : have;
             p.status[b] = served ? 0 : 1;
         }
-        __syncthreads();
-        for (int i = warp; i < min(kPlanThreads, p.B - b0); i += kPlanThreads / 32) {
-            int* row = p.table + static_cast<size_t>(b0 + i) * p.max_pages;
-            for (int c = s_used[i] + lane; c < s_total[i]; c += 32)
-                row[c] = p.free_pages[n_free - 1 - (s_first[i] + c - s_used[i])];
+        auto popped = [&](int i, int c) { return __ldg(p.free_pages + (n_free - 1 - (s_first[i] + c - s_used[i]))); };
+        plan_copy_runs(
+            s_used, s_total, rank * (kPlanThreads / 32) + (threadIdx.x >> 5), n_cta * (kPlanThreads / 32), n, popped,
+            [&](int i, int c, int page) { p.table[static_cast<size_t>(b0 + i) * p.max_pages + c] = page; });
+        if (SLOTS) {
+            for (int k = rank * kPlanThreads + threadIdx.x; k < n * p.L; k += n_cta * kPlanThreads) {
+                const int i = k / p.L, j = k - i * p.L;
+                int slot = -1;
+                if (j < s_rows[i]) {
+                    const int row = s_have[i] + j, c = row / p.page_size;
+                    const int page = c < s_used[i] ? p.table[static_cast<size_t>(b0 + i) * p.max_pages + c] : popped(i, c);
+                    if (page < 0 || page >= p.n_pages)
+                        atomicOr(&g_attn_err, kDevErrPage);
+                    else
+                        slot = page * p.page_size + row % p.page_size;
+                }
+                p.slots[static_cast<size_t>(b0) * p.L + k] = slot;
+            }
         }
         before += asked;
         taken += given;
     }
-    if (threadIdx.x == 0) *p.out_n_free = n_free - static_cast<int>(taken);
+    if (rank == 0 && threadIdx.x == 0) *p.out_n_free = n_free - static_cast<int>(taken);
 }
 
-// The slot of every new row, from the table and lengths attn_page_plan_kernel wrote.
-__global__ void __launch_bounds__(256) attn_page_slots_kernel(const PlanParams p) {
+// The slot of every new row, from the table and lengths attn_page_plan_kernel wrote: units of
+// kSlotRun rows of one request.
+constexpr int kSlotThreads = 256;
+constexpr int kSlotRun = 4 * kSlotThreads;
+
+__global__ void __launch_bounds__(kSlotThreads) attn_page_slots_kernel(const PlanParams p) {
     grid_dep_wait();
-    const size_t n = static_cast<size_t>(p.B) * p.L;
-    for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < n;
-         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-        const int b = static_cast<int>(i / p.L), j = static_cast<int>(i % p.L);
-        int slot = -1;
+    const int runs = (p.L + kSlotRun - 1) / kSlotRun;
+    const long long units = static_cast<long long>(p.B) * runs;
+    for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int b = static_cast<int>(unit / runs), j0 = static_cast<int>(unit % runs) * kSlotRun;
         const int want = p.new_lens[b];
-        if (p.status[b] == 0 && j < want) {
-            const int row = p.out_seqlens[b] - want + j;
-            const int page = p.table[static_cast<size_t>(b) * p.max_pages + row / p.page_size];
-            if (page < 0 || page >= p.n_pages)
-                atomicOr(&g_attn_err, kDevErrPage);
-            else
-                slot = page * p.page_size + row % p.page_size;
+        const int given = p.status[b] == 0 ? want : 0;
+        const int row0 = p.out_seqlens[b] - want;
+        const int* table = p.table + static_cast<size_t>(b) * p.max_pages;
+        int* slots = p.slots + static_cast<size_t>(b) * p.L;
+        int page[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * kSlotThreads + static_cast<int>(threadIdx.x);
+            page[u] = j < given ? table[(row0 + j) / p.page_size] : -1;
         }
-        p.slots[i] = slot;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * kSlotThreads + static_cast<int>(threadIdx.x);
+            int slot = -1;
+            if (j < given) {
+                if (page[u] < 0 || page[u] >= p.n_pages)
+                    atomicOr(&g_attn_err, kDevErrPage);
+                else
+                    slot = page[u] * p.page_size + (row0 + j) % p.page_size;
+            }
+            if (j < p.L) slots[j] = slot;
+        }
     }
 }
 
 // Pages past the rows a request keeps go back on the stack, requests and pages in order.
+// One CTA or a cluster, as attn_page_plan_kernel.
 __global__ void __launch_bounds__(kPlanThreads) attn_page_release_kernel(const PlanParams p) {
     __shared__ long long warp_sums[32];
     __shared__ int s_used[kPlanThreads], s_kept[kPlanThreads], s_first[kPlanThreads];
     const int n_free = plan_n_free(p);
+    const int rank = blockIdx.x, n_cta = gridDim.x;
     long long before = n_free;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
         int used = 0, kept = 0;
@@ -172,18 +261,19 @@ __global__ void __launch_bounds__(kPlanThreads) attn_page_release_kernel(const P
         s_used[threadIdx.x] = used;
         s_kept[threadIdx.x] = kept;
         s_first[threadIdx.x] = static_cast<int>(first);
-        __syncthreads();
-        for (int i = warp; i < min(kPlanThreads, p.B - b0); i += kPlanThreads / 32) {
-            const int* row = p.table + static_cast<size_t>(b0 + i) * p.max_pages;
-            for (int c = s_kept[i] + lane; c < s_used[i]; c += 32) {
-                if (row[c] < 0 || row[c] >= p.n_pages) atomicOr(&g_attn_err, kDevErrPage);
+        plan_sync();
+        plan_copy_runs(
+            s_kept, s_used, rank * (kPlanThreads / 32) + (threadIdx.x >> 5), n_cta * (kPlanThreads / 32),
+            min(kPlanThreads, p.B - b0),
+            [&](int i, int c) { return __ldg(p.table + static_cast<size_t>(b0 + i) * p.max_pages + c); },
+            [&](int i, int c, int page) {
+                if (page < 0 || page >= p.n_pages) atomicOr(&g_attn_err, kDevErrPage);
                 const long long at = static_cast<long long>(s_first[i]) + c - s_kept[i];
-                if (at < p.capacity) p.free_pages[at] = row[c];
-            }
-        }
+                if (at < p.capacity) p.free_pages[at] = page;
+            });
         before += gone;
     }
-    if (threadIdx.x == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
         if (before > p.capacity) atomicOr(&g_attn_err, kDevErrPage);
         *p.out_n_free = static_cast<int>(min(before, static_cast<long long>(p.capacity)));
     }
@@ -203,6 +293,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_page_release_kernel(const P
 // ---------------------------------------------------------------------------
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 2;       // rows of a thread in flight
+constexpr int kRopeTokens = 4;     // tokens of a CTA, where there are many
 constexpr int kCacheBf16 = 0;      // else ATTN_KV_E4M3 = 1, ATTN_KV_Q8_0 = 2
 
 struct RopeParams {
@@ -254,142 +346,173 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
-// One CTA per token: its rot / 2 angles once, then its Hq + 2 Hkv rows, D / 16 threads a
-// row, 16 elements a thread: the two halves of 8 pairs ("half": elements i and i + rot / 2
-// pair up) or 16 neighbours ("adjacent": elements 2i and 2i + 1).
-template <int D, int FMT, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) attn_rope_append_kernel(const RopeParams p) {
+// A CTA takes TOK tokens: their TOK x rot / 2 angles once, to shared memory, then their
+// TOK x (Hq + 2 Hkv) rows, D / 16 threads a row, 16 elements a thread: the two halves of 8
+// pairs ("half": elements i and i + rot / 2 pair up) or 16 neighbours ("adjacent": elements
+// 2i and 2i + 1).  A thread loads kRopeRows rows before it turns the first.
+template <int D, int FMT, bool ADJ, int TOK>
+__global__ void __launch_bounds__(kRopeThreads, 4) attn_rope_append_kernel(const RopeParams p) {
     constexpr int TPR = D / 16;                    // threads per row
     constexpr int RPP = kRopeThreads / TPR;        // rows per pass
-    __shared__ float2 turn[D / 2];
+    __shared__ float2 turn[TOK][D / 2];
+    __shared__ int s_outer[TOK], s_row[TOK];       // cache slab and row of a token (slab -1: not stored)
+    __shared__ size_t s_q[TOK];                    // row of q_out of its head 0
     __shared__ unsigned int amax[FMT == 2 ? RPP * (D / 32) : 1];
     const int N = p.B * p.L;
-    const int tok = blockIdx.x;
-    const int b = tok / p.L, l = tok % p.L;
-    for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads)
-        turn[i] = rope_turn(p.positions[static_cast<size_t>(rope_axis(p, i)) * N + tok], p.inv_freq[i]);
-    long long slot = p.slots[tok];
-    if (slot >= p.n_slots) {
-        if (threadIdx.x == 0) atomicOr(&g_attn_err, kDevErrPage);
-        slot = -1;
-    }
-    __syncthreads();
+    const int tok0 = blockIdx.x * TOK;
+    const int n_tok = min(TOK, N - tok0);
     const int sub = threadIdx.x % TPR, rloc = threadIdx.x / TPR;
     const int rows = p.Hq + 2 * p.Hkv;
-    for (int r0 = 0; r0 < rows; r0 += RPP) {
-        const int r = r0 + rloc;
-        const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv;
-        const bool on = r < rows && (is_q || slot >= 0);
-        const int head = is_q ? r : (is_k ? r - p.Hq : r - p.Hq - p.Hkv);
-        // element offsets of this thread's two runs of 8
-        const bool turned = (is_q || is_k) && sub * 16 < p.rot;
-        int ea = sub * 16, eb = ea + 8;
-        if (!ADJ && turned) {
-            ea = sub * 8;
-            eb = ea + p.rot / 2;
+    const int half = p.rot / 2;
+    if (threadIdx.x < n_tok) {
+        const int tok = tok0 + threadIdx.x;
+        int slot = p.slots[tok];
+        if (slot >= p.n_slots) {
+            atomicOr(&g_attn_err, kDevErrPage);
+            slot = -1;
         }
-        float xa[8], xb[8];
-        if (on) {
-            const __nv_bfloat16* src = is_q ? p.q + tok * p.q_tok : (is_k ? p.k + tok * p.k_tok : p.v + tok * p.v_tok);
-            src += static_cast<size_t>(head) * D;
-            unpack8(*reinterpret_cast<const uint4*>(src + ea), xa);
-            unpack8(*reinterpret_cast<const uint4*>(src + eb), xb);
-            if (turned) {
-                if (ADJ) {
+        s_outer[threadIdx.x] = slot < 0 ? -1 : slot / p.page_size;
+        s_row[threadIdx.x] = slot < 0 ? 0 : slot % p.page_size;
+        s_q[threadIdx.x] = static_cast<size_t>(tok / p.L) * p.Hq * p.L + tok % p.L;
+    }
+    for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
+        const int t = i / half, pair = i - t * half;
+        turn[t][pair] = rope_turn(p.positions[static_cast<size_t>(rope_axis(p, pair)) * N + tok0 + t], p.inv_freq[pair]);
+    }
+    __syncthreads();
+    // element offsets of this thread's two runs of 8, in a turned row and in V's
+    const bool turns = sub * 16 < p.rot;
+    const int va = sub * 16, vb = va + 8;
+    const int ta = !ADJ && turns ? sub * 8 : va, tb = !ADJ && turns ? ta + half : vb;
+    const int n_rows = n_tok * rows;
+    for (int r0 = rloc; r0 - rloc < n_rows; r0 += kRopeRows * RPP) {
+        uint4 ua[kRopeRows], ub[kRopeRows];
+        int tk[kRopeRows], rr[kRopeRows];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 ta = turn[sub * 8 + i / 2], tb = turn[sub * 8 + 4 + i / 2];
-                        const float a0 = xa[i], b0 = xb[i];
-                        xa[i] = a0 * ta.x - xa[i + 1] * ta.y;
-                        xa[i + 1] = xa[i + 1] * ta.x + a0 * ta.y;
-                        xb[i] = b0 * tb.x - xb[i + 1] * tb.y;
-                        xb[i + 1] = xb[i + 1] * tb.x + b0 * tb.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 t = turn[sub * 8 + i];
-                        const float a0 = xa[i];
-                        xa[i] = a0 * t.x - xb[i] * t.y;
-                        xb[i] = xb[i] * t.x + a0 * t.y;
-                    }
+        for (int u = 0; u < kRopeRows; ++u) {
+            const int it = r0 + u * RPP;
+            tk[u] = -1;
+            if (it < n_rows) {
+                const int t = TOK == 1 ? 0 : it / rows, r = it - t * rows;
+                const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
+                if (is_q || s_outer[t] >= 0) {
+                    const long long tok = tok0 + t;
+                    const __nv_bfloat16* src = is_q ? p.q + tok * p.q_tok + static_cast<size_t>(r) * D
+                                               : is_v ? p.v + tok * p.v_tok + static_cast<size_t>(r - p.Hq - p.Hkv) * D
+                                                      : p.k + tok * p.k_tok + static_cast<size_t>(r - p.Hq) * D;
+                    tk[u] = t;
+                    rr[u] = r;
+                    ua[u] = __ldg(reinterpret_cast<const uint4*>(src + (is_v ? va : ta)));
+                    ub[u] = __ldg(reinterpret_cast<const uint4*>(src + (is_v ? vb : tb)));
                 }
             }
         }
-        if (on && is_q) {
-            __nv_bfloat16* dst = p.q_out + ((static_cast<size_t>(b) * p.Hq + head) * p.L + l) * D;
-            *reinterpret_cast<uint4*>(dst + ea) = pack8(xa);
-            *reinterpret_cast<uint4*>(dst + eb) = pack8(xb);
-        }
-        const bool store = on && !is_q;
-        // row of the cache: [outer, Hkv, page_size, D]
-        size_t crow = 0;
-        if (store)
-            crow = (static_cast<size_t>(slot / p.page_size) * p.Hkv + head) * p.page_size + slot % p.page_size;
-        if constexpr (FMT == kCacheBf16) {
-            if (store) {
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_k ? p.k_cache : p.v_cache) + crow * D;
+#pragma unroll
+        for (int u = 0; u < kRopeRows; ++u) {
+            const bool on = tk[u] >= 0;
+            const int t = on ? tk[u] : 0, r = on ? rr[u] : 0;
+            const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
+            const int ea = is_v ? va : ta, eb = is_v ? vb : tb;
+            float xa[8], xb[8];
+            if (on) {
+                unpack8(ua[u], xa);
+                unpack8(ub[u], xb);
+                if (turns && !is_v) {
+                    if (ADJ) {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const float2 w = turn[t][sub * 8 + i / 2], z = turn[t][sub * 8 + 4 + i / 2];
+                            const float a0 = xa[i], b0 = xb[i];
+                            xa[i] = a0 * w.x - xa[i + 1] * w.y;
+                            xa[i + 1] = xa[i + 1] * w.x + a0 * w.y;
+                            xb[i] = b0 * z.x - xb[i + 1] * z.y;
+                            xb[i + 1] = xb[i + 1] * z.x + b0 * z.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 w = turn[t][sub * 8 + i];
+                            const float a0 = xa[i];
+                            xa[i] = a0 * w.x - xb[i] * w.y;
+                            xb[i] = xb[i] * w.x + a0 * w.y;
+                        }
+                    }
+                }
+            }
+            if (on && is_q) {
+                __nv_bfloat16* dst = p.q_out + (s_q[t] + static_cast<size_t>(r) * p.L) * D;
                 *reinterpret_cast<uint4*>(dst + ea) = pack8(xa);
                 *reinterpret_cast<uint4*>(dst + eb) = pack8(xb);
             }
-        } else if constexpr (FMT == 1) {
-            // E4M3 of x / scale, rounded to the nearest, saturating at 448
-            if (store) {
-                uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) + crow * D;
-                const float sc = static_cast<const float*>(is_k ? p.k_scale : p.v_scale)[head];
-                auto codes = [&](const float* x) {
-                    uint32_t w[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h] / sc, x[4 * h + 1] / sc), __NV_SATFINITE, __NV_E4M3);
-                        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h + 2] / sc, x[4 * h + 3] / sc), __NV_SATFINITE, __NV_E4M3);
-                        w[h] = lo | (hi << 16);
-                    }
-                    return make_uint2(w[0], w[1]);
-                };
-                *reinterpret_cast<uint2*>(dst + ea) = codes(xa);
-                *reinterpret_cast<uint2*>(dst + eb) = codes(xb);
-            }
-        } else {
-            // q8_0: per 32 elements the scale fp16(max |x| / 127), codes rint(x / scale).  The
-            // 8-element runs of a block meet in shared memory: |x| as bits orders like |x|, NaN above all.
-            unsigned int* am = amax + rloc * (D / 32);
-            if (sub < D / 32) am[sub] = 0u;
-            __syncwarp();
-            if (store) {
-                unsigned int ma = 0u, mb = 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ma = max(ma, __float_as_uint(fabsf(xa[i])));
-                    mb = max(mb, __float_as_uint(fabsf(xb[i])));
+            const bool store = on && !is_q;
+            const int head = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
+            // row of the cache: [outer, Hkv, page_size, D]
+            const size_t crow = store ? (static_cast<size_t>(s_outer[t]) * p.Hkv + head) * p.page_size + s_row[t] : 0;
+            if constexpr (FMT == kCacheBf16) {
+                if (store) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + crow * D;
+                    *reinterpret_cast<uint4*>(dst + ea) = pack8(xa);
+                    *reinterpret_cast<uint4*>(dst + eb) = pack8(xb);
                 }
-                atomicMax(am + ea / 32, ma);
-                atomicMax(am + eb / 32, mb);
-            }
-            __syncwarp();
-            if (store) {
-                int8_t* dst = static_cast<int8_t*>(is_k ? p.k_cache : p.v_cache) + crow * D;
-                __half* scales = static_cast<__half*>(is_k ? p.k_scale : p.v_scale) + crow * (D / 32);
-                auto scale_of = [&](int e) {
-                    const float m = __uint_as_float(am[e / 32]) / 127.0f;
-                    return __float2half_rn(m > 65504.0f ? 65504.0f : m);      // NaN stays
-                };
-                auto codes = [&](const float* x, float sc) {
-                    uint32_t w[2] = {0u, 0u};
+            } else if constexpr (FMT == 1) {
+                // E4M3 of x / scale, rounded to the nearest, saturating at 448
+                if (store) {
+                    uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + crow * D;
+                    const float sc = __ldg(static_cast<const float*>(is_v ? p.v_scale : p.k_scale) + head);
+                    auto codes = [&](const float* x) {
+                        uint32_t w[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h] / sc, x[4 * h + 1] / sc), __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h + 2] / sc, x[4 * h + 3] / sc), __NV_SATFINITE, __NV_E4M3);
+                            w[h] = lo | (hi << 16);
+                        }
+                        return make_uint2(w[0], w[1]);
+                    };
+                    *reinterpret_cast<uint2*>(dst + ea) = codes(xa);
+                    *reinterpret_cast<uint2*>(dst + eb) = codes(xb);
+                }
+            } else {
+                // q8_0: per 32 elements the scale fp16(max |x| / 127), codes rint(x / scale).  The
+                // 8-element runs of a block meet in shared memory: |x| as bits orders like |x|, NaN above all.
+                unsigned int* am = amax + rloc * (D / 32);
+                if (sub < D / 32) am[sub] = 0u;
+                __syncwarp();
+                if (store) {
+                    unsigned int ma = 0u, mb = 0u;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float c = sc > 0.0f ? fminf(fmaxf(rintf(x[i] / sc), -127.0f), 127.0f) : 0.0f;
-                        w[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xffu) << (8 * (i & 3));
+                        ma = max(ma, __float_as_uint(fabsf(xa[i])));
+                        mb = max(mb, __float_as_uint(fabsf(xb[i])));
                     }
-                    return make_uint2(w[0], w[1]);
-                };
-                const __half sa = scale_of(ea), sb = scale_of(eb);
-                *reinterpret_cast<uint2*>(dst + ea) = codes(xa, __half2float(sa));
-                *reinterpret_cast<uint2*>(dst + eb) = codes(xb, __half2float(sb));
-                if (ea % 32 == 0) scales[ea / 32] = sa;
-                if (eb % 32 == 0) scales[eb / 32] = sb;
+                    atomicMax(am + ea / 32, ma);
+                    atomicMax(am + eb / 32, mb);
+                }
+                __syncwarp();
+                if (store) {
+                    int8_t* dst = static_cast<int8_t*>(is_v ? p.v_cache : p.k_cache) + crow * D;
+                    __half* scales = static_cast<__half*>(is_v ? p.v_scale : p.k_scale) + crow * (D / 32);
+                    auto scale_of = [&](int e) {
+                        const float m = __uint_as_float(am[e / 32]) / 127.0f;
+                        return __float2half_rn(m > 65504.0f ? 65504.0f : m);      // NaN stays
+                    };
+                    auto codes = [&](const float* x, float sc) {
+                        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float c = sc > 0.0f ? fminf(fmaxf(rintf(x[i] / sc), -127.0f), 127.0f) : 0.0f;
+                            w[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xffu) << (8 * (i & 3));
+                        }
+                        return make_uint2(w[0], w[1]);
+                    };
+                    const __half sa = scale_of(ea), sb = scale_of(eb);
+                    *reinterpret_cast<uint2*>(dst + ea) = codes(xa, __half2float(sa));
+                    *reinterpret_cast<uint2*>(dst + eb) = codes(xb, __half2float(sb));
+                    if (ea % 32 == 0) scales[ea / 32] = sa;
+                    if (eb % 32 == 0) scales[eb / 32] = sb;
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
 }
