@@ -189,13 +189,13 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned b
 // The split combine: one warp per row (four rows per CTA) when rows have few
 // splits, four warps per row when they have more than 16 (their reads then take
 // four times fewer dependent rounds).
-template <int D, bool F32, bool NANLSE = false>
+template <int D, bool F32>
 int launch_combine(const DecodeParams& prm, void* out, float* lse, int rows, cudaStream_t stream) {
     const cudaError_t e =
         (prm.n_splits > 16)
-            ? launch_dependent(attn_decode_combine_kernel<D, F32, 4, NANLSE>, static_cast<unsigned>(rows), 128u, stream, prm,
+            ? launch_dependent(attn_decode_combine_kernel<D, F32, 4>, static_cast<unsigned>(rows), 128u, stream, prm,
                                out, lse)
-            : launch_dependent(attn_decode_combine_kernel<D, F32, 1, NANLSE>, static_cast<unsigned>((rows + 3) / 4), 128u,
+            : launch_dependent(attn_decode_combine_kernel<D, F32, 1>, static_cast<unsigned>((rows + 3) / 4), 128u,
                                stream, prm, out, lse);
     if (e != cudaSuccess)
         return fail(ATTN_ERR_CUDA, "attn_decode_combine_kernel launch failed: %s", cudaGetErrorString(e));

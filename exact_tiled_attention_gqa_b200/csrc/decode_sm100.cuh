@@ -412,9 +412,7 @@ __global__ void __maxnreg__(200)
 // used, so a row with up to WPR * kChunk splits costs one round trip to memory.
 // The warps' sums meet in shared memory.
 // F32: out is fp32 [rows, D] instead of bf16 (a partial result that is merged later).
-// NANLSE: a row whose scores hold NaN has LSE NaN, as its out (else -inf, as a row
-// without keys).
-template <int D, bool F32 = false, int WPR = 1, bool NANLSE = false>
+template <int D, bool F32 = false, int WPR = 1>
 __global__ void __launch_bounds__(128)
     attn_decode_combine_kernel(const DecodeParams p, void* out_ptr, float* lse) {
     grid_dep_wait();   // launched as a programmatic dependent of the split kernel
@@ -504,8 +502,7 @@ __global__ void __launch_bounds__(128)
             *reinterpret_cast<uint32_t*>(o + i) = v2;
         }
     }
-    const bool some = NANLSE ? !(Lsum == 0.0f) : Lsum > 0.0f;
-    if (lse != nullptr && lane == 0) lse[row] = some ? (M + __log2f(Lsum)) * kLn2 : -INFINITY;
+    if (lse != nullptr && lane == 0) lse[row] = (Lsum > 0.0f) ? (M + __log2f(Lsum)) * kLn2 : -INFINITY;
 }
 
 // Merge of decode results over disjoint sets of cache rows (KV parallelism: each

@@ -11,9 +11,12 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // ---- tree attention ----
 
 struct TreeLayout {
-    int n_mblk = 0, chunk = 0, n_splits = 0;
-    size_t lse_off = 0, total = 0;
+    int n_mblk = 0, n_ranges = 0;
+    size_t lse_off = 0, tiles_off = 0, total = 0;
 };
+
+// A range has at least this many 64-row tiles.
+constexpr int kTreeMinTiles = 2;
 
 // Sizes the calls accept (the workspace size of others is 0).
 bool tree_sizes_ok(int B, int Hq, int Hkv, int T, int Lmax, int D) {
@@ -22,24 +25,27 @@ bool tree_sizes_ok(int B, int Hq, int Hkv, int T, int Lmax, int D) {
            static_cast<long long>(B) * Hq * T <= 0x7fffffffLL;
 }
 
+// Depends on the arguments only: 148 SMs, one CTA (D = 256) or two on each.
 TreeLayout tree_layout(int B, int Hq, int Hkv, int T, int Lmax, int D) {
     TreeLayout t;
     const long long rg = static_cast<long long>(Hq / Hkv) * T;
     t.n_mblk = static_cast<int>((rg + 127) / 128);
-    t.chunk = decode_chunk(B, Hkv * t.n_mblk, Lmax, true, D);
-    t.n_splits = (Lmax + t.chunk - 1) / t.chunk;
-    const size_t rows = static_cast<size_t>(B) * Hq * T * t.n_splits;
+    const long long tiles = static_cast<long long>(B) * Hkv * ((Lmax + 63LL) / 64);
+    const long long ctas = D == 256 ? 148 : 296;
+    t.n_ranges = static_cast<int>(std::max(1LL, std::min(ctas / t.n_mblk, (tiles + kTreeMinTiles - 1) / kTreeMinTiles)));
+    const size_t rows = static_cast<size_t>(t.n_ranges) * t.n_mblk * 2 * static_cast<size_t>(std::min(128LL, rg));
     t.lse_off = align256(rows * D * sizeof(float));
-    t.total = t.lse_off + align256(rows * sizeof(float));
+    t.tiles_off = t.lse_off + align256(rows * sizeof(float));
+    t.total = t.tiles_off + align256((static_cast<size_t>(B) + 1) * sizeof(long long));
     return t;
 }
 
 template <int D>
-int launch_tree(const void* q, const void* kc, const void* vc, TreeParams tp, const TreeLayout& lay, void* out,
-                float* lse, cudaStream_t stream) {
+int launch_tree(const void* q, const void* kc, const void* vc, const TreeParams& tp, const TreeLayout& lay,
+                cudaStream_t stream) {
     static int smem_done[64];
-    using L = DecodeTcSmem<D>;
-    DecodeParams& prm = tp.d;
+    using L = TreeSmem<D>;
+    const DecodeParams& prm = tp.d;
     const uint64_t rows = prm.block_table ? static_cast<uint64_t>(prm.page_size) : static_cast<uint64_t>(prm.Lmax);
     const uint64_t outer = static_cast<uint64_t>(prm.block_table ? prm.n_pages : prm.B) * prm.Hkv;
     const int box = std::min(128, prm.G * prm.Lq);
@@ -50,10 +56,16 @@ int launch_tree(const void* q, const void* kc, const void* vc, TreeParams tp, co
     if ((st = encode_bf16_3d(&tk, kc, D, rows, outer, 64, kDecKT, 1, "k_cache")) != ATTN_OK) return st;
     if ((st = encode_bf16_3d(&tv, vc, D, rows, outer, 64, kDecKT, 1, "v_cache")) != ATTN_OK) return st;
     if ((st = ensure_smem(attn_tree_kernel<D>, L::kAlloc, smem_done)) != ATTN_OK) return st;
-    dim3 grid(prm.n_splits, prm.Hkv * tp.n_mblk, prm.B);
-    attn_tree_kernel<D><<<grid, kDtcThreads, L::kAlloc, stream>>>(tq, tk, tv, tp);
+    attn_tree_kernel<D><<<static_cast<unsigned>(lay.n_ranges) * lay.n_mblk, kDtcThreads, L::kAlloc, stream>>>(tq, tk, tv, tp);
     if ((st = check_launch("attn_tree_kernel")) != ATTN_OK) return st;
-    return launch_combine<D, false, true>(prm, out, lse, prm.B * prm.Hq * prm.Lq, stream);
+    const int q_rows = prm.B * prm.Hq * prm.Lq;
+    // a pair over more than 16 ranges: four warps a row
+    const cudaError_t e =
+        lay.n_ranges > 16LL * prm.B * prm.Hkv
+            ? launch_dependent(attn_tree_combine_kernel<D, 4>, static_cast<unsigned>(q_rows), 128u, stream, tp)
+            : launch_dependent(attn_tree_combine_kernel<D, 1>, static_cast<unsigned>((q_rows + 3) / 4), 128u, stream, tp);
+    if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "attn_tree_combine_kernel launch failed: %s", cudaGetErrorString(e));
+    return check_launch("attn_tree_combine_kernel");
 }
 
 int tree_checked(const void* q, const void* kc, const void* vc, const int32_t* block_table, const int32_t* seqlens,
@@ -70,9 +82,6 @@ int tree_checked(const void* q, const void* kc, const void* vc, const int32_t* b
     if (!tree_sizes_ok(B, Hq, Hkv, T, Lmax, D)) return fail(ATTN_ERR_UNSUPPORTED, "B*Hq*T or Lmax too large");
     if (B == 0) return ok();
     const TreeLayout lay = tree_layout(B, Hq, Hkv, T, Lmax, D);
-    if (lay.n_splits > 65535 || static_cast<long long>(Hkv) * lay.n_mblk > 65535 || B > 65535)
-        return fail(ATTN_ERR_UNSUPPORTED, "tree attention grid (%d, %lld, %d) exceeds launch limits", lay.n_splits,
-                    static_cast<long long>(Hkv) * lay.n_mblk, B);
     if (!workspace || workspace_bytes < lay.total)
         return fail(ATTN_ERR_WORKSPACE, "tree attention workspace needs %zu bytes, got %zu", lay.total,
                     workspace ? workspace_bytes : static_cast<size_t>(0));
@@ -94,9 +103,13 @@ int tree_checked(const void* q, const void* kc, const void* vc, const int32_t* b
     prm.page_size = page_size;
     prm.max_pages = max_pages;
     prm.n_pages = n_pages;
-    prm.chunk = lay.chunk;
-    prm.n_splits = lay.n_splits;
+    prm.chunk = prm.n_splits = 0;
     prm.scale_log2 = scale * kLog2e;
+    tp.out = static_cast<__nv_bfloat16*>(out);
+    tp.lse = lse;
+    tp.tiles_before = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + lay.tiles_off);
+    tp.n_ranges = lay.n_ranges;
+    tp.min_tiles = kTreeMinTiles;
     tp.mask = tree_mask;
     tp.W = (T + 31) / 32;
     tp.mask_batch = mask_per_seq ? static_cast<size_t>(T) * tp.W : 0;
@@ -104,9 +117,9 @@ int tree_checked(const void* q, const void* kc, const void* vc, const int32_t* b
     tp.v = static_cast<const __nv_bfloat16*>(vc);
     tp.n_mblk = lay.n_mblk;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = (D == 256)   ? launch_tree<256>(q, kc, vc, tp, lay, out, lse, s)
-         : (D == 128) ? launch_tree<128>(q, kc, vc, tp, lay, out, lse, s)
-                      : launch_tree<64>(q, kc, vc, tp, lay, out, lse, s);
+    st = (D == 256)   ? launch_tree<256>(q, kc, vc, tp, lay, s)
+         : (D == 128) ? launch_tree<128>(q, kc, vc, tp, lay, s)
+                      : launch_tree<64>(q, kc, vc, tp, lay, s);
     return st == ATTN_OK ? ok() : st;
 }
 
@@ -248,7 +261,8 @@ extern "C" int attn_page_release(const int32_t* seqlens, const int32_t* keep_len
 
 namespace attn {
 namespace {
-// Four tokens a CTA once that leaves four CTAs to each of 148 SMs, else one.
+// Eight tokens a CTA once that leaves four CTAs to each of 148 SMs, else one (and
+// where a token's rows are so many that the kernel's division would not be exact).
 constexpr long long kRopeManyTokens = 148LL * 4 * kRopeTokens;
 
 template <int D, int FMT, int TOK>
@@ -262,7 +276,7 @@ int launch_rope_tokens(const RopeParams& p, bool adjacent, cudaStream_t s) {
 }
 template <int D, int FMT>
 int launch_rope(const RopeParams& p, bool adjacent, cudaStream_t s) {
-    return static_cast<long long>(p.B) * p.L >= kRopeManyTokens ? launch_rope_tokens<D, FMT, kRopeTokens>(p, adjacent, s)
+    return static_cast<long long>(p.B) * p.L >= kRopeManyTokens && p.Hq + 2 * p.Hkv < 16384 ? launch_rope_tokens<D, FMT, kRopeTokens>(p, adjacent, s)
                                                                 : launch_rope_tokens<D, FMT, 1>(p, adjacent, s);
 }
 template <int D>
@@ -342,6 +356,7 @@ extern "C" int attn_rope_append(const void* q, const void* k, const void* v, lon
     p.n_axes = n_axes;
     for (int a = 0; a < 4; ++a) p.sections[a] = a < n_axes ? sections[a] : 0;
     p.cycle = axis_cycle ? 1 : 0;
+    p.row_div = static_cast<unsigned int>(0xffffffffu / static_cast<unsigned int>(Hq + 2 * Hkv)) + 1u;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool adj = adjacent != 0;
     const int st = (D == 256)   ? launch_rope_fmt<256>(p, kv_format, adj, s)

@@ -382,6 +382,25 @@ def test_tree_against_plain(D, Hq, Hkv, T, lens, sizes, kind):
     assert torch.equal(again, out) and torch.equal(lagain, lse)
 
 
+@pytest.mark.parametrize("D,B,Hq,Hkv,T,top", [(64, 150, 8, 8, 3, 200), (128, 120, 16, 8, 5, 300), (256, 100, 8, 8, 2, 260), (128, 40, 40, 8, 30, 150),
+                                             (64, 300, 4, 4, 1, 140)])
+def test_tree_many_short_sequences(D, B, Hq, Hkv, T, top):
+    """More (sequence, KV head) pairs than CTAs: a CTA takes several, whole or in part, some sequences are empty."""
+    r = random.Random(B)
+    lens = [r.choice([0, 1, 63, 64, 65, r.randrange(0, top)]) for _ in range(B)]
+    sizes = [min(n, r.randrange(0, T + 1)) for n in lens]
+    q, masks, rows = _tree_case(lens, sizes, Hq, Hkv, T, D, "tree", B)
+    want = _reference(q, masks, rows, lens, sizes, 1 / math.sqrt(D))
+    words, sl, tl = attn.pack_tree_mask(masks).cuda(), i32(lens), i32(sizes)
+    kp, vp, table = (t.cuda() for t in _paged(rows, 64, B))
+    out, lse = attn.decode_tree_paged(q.cuda(), kp, vp, table, sl, words, tree_lens=tl)
+    assert attn.device_error(reset=True) == 0
+    ref.check_tree(out, lse, want, f"B{B} D{D}")
+    kc, vc = (t.cuda() for t in _contiguous(rows, max(lens)))
+    out, lse = attn.decode_tree(q.cuda(), kc, vc, sl, words, tree_lens=tl)
+    ref.check_tree(out, lse, want, f"B{B} D{D} contiguous")
+
+
 def test_tree_defaults_shared_mask_results_and_scale():
     """tree_lens None is T for all; a [T,W] mask serves every sequence; out, lse and workspace are the caller's."""
     Hq, Hkv, T, D, lens = 8, 4, 20, 128, [300, 20, 77]
