@@ -221,6 +221,45 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         : "memory");
 }
 
+// umma_ss, umma_ts and umma_commit by a whole convergent warp, of which the thread
+// with `leader` != 0 issues: the operands' arithmetic stays outside the branch, where
+// it is the same for all threads and the MMA can take it from uniform registers.
+__device__ __forceinline__ void umma_ss_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        "  .reg .pred p, q;\n"
+        "  setp.ne.b32 p, %4, 0;\n"
+        "  setp.ne.b32 q, %5, 0;\n"
+        "  @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_ts_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        "  .reg .pred p, q;\n"
+        "  setp.ne.b32 p, %4, 0;\n"
+        "  setp.ne.b32 q, %5, 0;\n"
+        "  @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n"
+        "  .reg .pred q;\n"
+        "  setp.ne.b32 q, %1, 0;\n"
+        "  @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(bar), "r"(leader)
+        : "memory");
+}
+
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 accumulator, dense.
 //   bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format
 //   (1 = bf16), 15 A major (0 = K), 16 B major (1 = MN), 17-22 N >> 3,

@@ -15,9 +15,6 @@ struct TreeLayout {
     size_t lse_off = 0, tiles_off = 0, total = 0;
 };
 
-// A range has at least this many 64-row tiles.
-constexpr int kTreeMinTiles = 2;
-
 // Sizes the calls accept (the workspace size of others is 0).
 bool tree_sizes_ok(int B, int Hq, int Hkv, int T, int Lmax, int D) {
     return B >= 0 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && T >= 1 && T <= kTreeMaxNodes && Lmax >= 1 &&
@@ -31,8 +28,8 @@ TreeLayout tree_layout(int B, int Hq, int Hkv, int T, int Lmax, int D) {
     const long long rg = static_cast<long long>(Hq / Hkv) * T;
     t.n_mblk = static_cast<int>((rg + 127) / 128);
     const long long tiles = static_cast<long long>(B) * Hkv * ((Lmax + 63LL) / 64);
-    const long long ctas = D == 256 ? 148 : 296;
-    t.n_ranges = static_cast<int>(std::max(1LL, std::min(ctas / t.n_mblk, (tiles + kTreeMinTiles - 1) / kTreeMinTiles)));
+    const long long ctas = 148LL * (D == 256 ? TreeCfg<256>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
+    t.n_ranges = static_cast<int>(std::max(1LL, std::min(ctas / t.n_mblk, (tiles + 1) / 2)));
     const size_t rows = static_cast<size_t>(t.n_ranges) * t.n_mblk * 2 * static_cast<size_t>(std::min(128LL, rg));
     t.lse_off = align256(rows * D * sizeof(float));
     t.tiles_off = t.lse_off + align256(rows * sizeof(float));
@@ -44,7 +41,7 @@ template <int D>
 int launch_tree(const void* q, const void* kc, const void* vc, const TreeParams& tp, const TreeLayout& lay,
                 cudaStream_t stream) {
     static int smem_done[64];
-    using L = TreeSmem<D>;
+    using L = TreeCfg<D>;
     const DecodeParams& prm = tp.d;
     const uint64_t rows = prm.block_table ? static_cast<uint64_t>(prm.page_size) : static_cast<uint64_t>(prm.Lmax);
     const uint64_t outer = static_cast<uint64_t>(prm.block_table ? prm.n_pages : prm.B) * prm.Hkv;
@@ -56,14 +53,15 @@ int launch_tree(const void* q, const void* kc, const void* vc, const TreeParams&
     if ((st = encode_bf16_3d(&tk, kc, D, rows, outer, 64, kDecKT, 1, "k_cache")) != ATTN_OK) return st;
     if ((st = encode_bf16_3d(&tv, vc, D, rows, outer, 64, kDecKT, 1, "v_cache")) != ATTN_OK) return st;
     if ((st = ensure_smem(attn_tree_kernel<D>, L::kAlloc, smem_done)) != ATTN_OK) return st;
-    attn_tree_kernel<D><<<static_cast<unsigned>(lay.n_ranges) * lay.n_mblk, kDtcThreads, L::kAlloc, stream>>>(tq, tk, tv, tp);
+    attn_tree_kernel<D><<<static_cast<unsigned>(lay.n_ranges) * lay.n_mblk, L::kThreads, L::kAlloc, stream>>>(tq, tk, tv, tp);
     if ((st = check_launch("attn_tree_kernel")) != ATTN_OK) return st;
-    const int q_rows = prm.B * prm.Hq * prm.Lq;
-    // a pair over more than 16 ranges: four warps a row
+    const long long pairs = static_cast<long long>(prm.B) * prm.Hkv, rows_per_pair = static_cast<long long>(prm.G) * prm.Lq;
+    const long long slices = (rows_per_pair + kTreeCombineRows - 1) / kTreeCombineRows;
+    // a pair over more than 4 ranges: a CTA for each row
     const cudaError_t e =
-        lay.n_ranges > 16LL * prm.B * prm.Hkv
-            ? launch_dependent(attn_tree_combine_kernel<D, 4>, static_cast<unsigned>(q_rows), 128u, stream, tp)
-            : launch_dependent(attn_tree_combine_kernel<D, 1>, static_cast<unsigned>((q_rows + 3) / 4), 128u, stream, tp);
+        lay.n_ranges > 4 * pairs
+            ? launch_dependent(attn_tree_combine_many_kernel<D>, static_cast<unsigned>(pairs * rows_per_pair), 128u, stream, tp)
+            : launch_dependent(attn_tree_combine_kernel<D>, static_cast<unsigned>(pairs * slices), 128u, stream, tp);
     if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "attn_tree_combine_kernel launch failed: %s", cudaGetErrorString(e));
     return check_launch("attn_tree_combine_kernel");
 }
@@ -109,7 +107,6 @@ int tree_checked(const void* q, const void* kc, const void* vc, const int32_t* b
     tp.lse = lse;
     tp.tiles_before = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + lay.tiles_off);
     tp.n_ranges = lay.n_ranges;
-    tp.min_tiles = kTreeMinTiles;
     tp.mask = tree_mask;
     tp.W = (T + 31) / 32;
     tp.mask_batch = mask_per_seq ? static_cast<size_t>(T) * tp.W : 0;

@@ -12,15 +12,20 @@
 // A row that sees nothing (an empty mask on an empty context, a node >= n_b)
 // gets O = 0 and LSE = -inf.
 //
-// The G x T query rows of a KV head are cut into blocks of 128, the M rows of the MMAs
-// (S = Q K^T and O += P V on 64-row tiles, as attn_decode_tc_kernel: two S buffers, P over
-// S in TMEM, lazy maximum).  The work is balanced from the lengths on the device: the 64-row
-// tiles of all (sequence, KV head) pairs in one line are cut into equal ranges, one CTA for
-// each range and query block, as many CTAs as the GPU holds at once.  A CTA walks its range
-// segment by segment (a segment: the part of one pair's tiles in the range); the CTAs of one
-// range read the same K and V side by side, so all but one of them find them in the L2.  A
-// segment that is a whole pair writes the result; the others write a normalised partial (at
-// most two a CTA) that attn_tree_combine_kernel merges.  The loads run on across segments.
+// The G x T query rows of a KV head are cut into blocks of 128, the M rows of the MMAs.  The
+// work is balanced from the lengths on the device: the tiles of all (sequence, KV head) pairs
+// in one line are cut into equal ranges, one CTA for each range and query block, as many CTAs
+// as the GPU holds at once.  A CTA walks its range segment by segment (a segment: the part of
+// one pair's tiles in the range); the CTAs of one range read the same K and V side by side, so
+// all but one of them find them in the L2.  A segment that is a whole pair writes the result;
+// the others write a normalised partial (at most two a CTA) that a combine kernel merges.  The
+// loads run on across segments.
+//
+// Per tile of 64 cache rows S = Q K^T, P = 2^(S scale log2 e - m) and O += P V, with two S
+// buffers, so that S of the next tile is computed under the softmax of this one, as
+// attn_decode_tc_kernel.  D = 64 and 128: Q in shared memory, two CTAs on an SM.  D = 256: O
+// takes half the TMEM, one CTA on an SM; Q lies in TMEM, which leaves its 64 KB of shared
+// memory to K and V.
 //
 // The mask costs nothing over the committed rows: only a tile that reaches past c builds the
 // 64 visibility bits of its rows, each thread (one query row) shifting them out of its own
@@ -55,10 +60,13 @@ struct TreeParams {
     int W;                       // words per mask row, (T + 31) / 32
     int n_mblk;                  // 128-row blocks of a KV head's G x T query rows
     int n_ranges;
-    int min_tiles;               // a range is no shorter
 };
 
-__device__ __forceinline__ int tree_tiles(int seqlen) { return seqlen / 64 + (seqlen % 64 != 0); }
+// Tiles of a sequence (rows of a tile: TreeCfg<D>::kTile).
+template <int TILE>
+__device__ __forceinline__ int tree_tiles(int seqlen) {
+    return seqlen / TILE + (seqlen % TILE != 0);
+}
 
 // Row r of the partial that range `range` wrote for query block mblk in slot 0 (its first
 // segment) or 1 (its last).
@@ -116,7 +124,7 @@ __device__ __forceinline__ size_t tree_cache_row(const DecodeParams& p, int b, i
 template <typename T>
 __device__ __noinline__ void tree_add_nonfinite(const TreeParams& tp, int b, int g, const uint32_t* words, int ctx,
                                                 int k_begin, int k_end, int D, T* dst) {
-    for (int row = max(ctx, k_begin); row < k_end; ++row) {
+    for (int row = max(max(ctx, 0), k_begin); row < k_end; ++row) {
         const int j = row - ctx;
         if (!(words[j >> 5] >> (j & 31) & 1u)) continue;
         const __nv_bfloat16* src = tp.v + tree_cache_row(tp.d, b, g, row) * D;
@@ -133,13 +141,36 @@ __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t x) {
 }
 
 template <int D>
-struct TreeSmem : DecodeTcSmem<D> {
-    using B = DecodeTcSmem<D>;
-    static constexpr int kNumBars = B::kNumBars + 1;                  // and q_empty
-    static constexpr int kMiscOff = B::kBarOff + kNumBars * 8;        // tmem base, abort flag, patched[2]
-    static constexpr int kTagOff = kMiscOff + 16;
-    static constexpr int kAlloc = kTagOff + 4 * B::kStages + 1024;
-    static_assert(kAlloc <= 232448, "dynamic shared memory per CTA");
+struct TreeCfg {
+    static constexpr int kKB = D / 64;
+    static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+    static constexpr bool kQTmem = D == 256;
+    static constexpr int kTile = 64;                          // cache rows of a tile
+    static constexpr int kThreads = 192;                      // softmax warps 0-3, producer, MMA issuer
+    static constexpr int kProducerWarp = 4;
+    static constexpr int kMmaWarp = 5;
+    // TMEM columns: S0, S1 (P over the first half of each), Q (D = 256), O
+    static constexpr uint32_t kTmemCols = D == 256 ? 512 : 256;
+    static constexpr uint32_t kTmemQ = 128, kTmemO = D == 256 ? 256 : 128;
+    // shared memory: Q as 128 rows x 128 bytes per 64 columns, then the ring of K and V tiles
+    static constexpr int kQBlockBytes = 128 * 128;
+    static constexpr int kQBytes = kQTmem ? 0 : 128 * D * 2;
+    static constexpr int kBlockBytes = kTile * 128;           // a tile's rows x 128 bytes per 64 columns
+    static constexpr int kTileBytes = kTile * D * 2;
+    // as many tiles as fit beside Q when kCtasPerSm CTAs share the SM's 228 KB (1 KB reserved per
+    // CTA, 1 KB alignment slack, 1 KB for what follows the ring), at most 16
+    static constexpr int kStagesFit = (233472 / kCtasPerSm - 3072 - kQBytes) / kTileBytes;
+    static constexpr int kStages = kStagesFit > 16 ? 16 : kStagesFit;
+    static constexpr int kKVOff = kQBytes;
+    static constexpr int kBarOff = kKVOff + kStages * kTileBytes;
+    // q_full, q_empty, full[S], empty[S], s_full[2], p_full[2], drain
+    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 1;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem base, abort flag, patched[2]
+    static constexpr int kTagOff = kMiscOff + 16;             // debug builds: ring entry -> item
+    static constexpr int kAlloc = kTagOff + 4 * kStages + 1024;
+    static_assert(kTagOff + 4 * kStages - kBarOff <= 768, "barriers and flags");
+    static_assert(kAlloc <= 232448 - 256, "dynamic shared memory per CTA");
+    static_assert(kStages >= 4, "ring too shallow");
 };
 
 // Part of one (sequence, KV head) pair's tiles in a CTA's range.
@@ -151,7 +182,8 @@ struct TreeSeg {
     int n;                    // segments before it
 };
 
-// The segment at s.x; false when the range is done.  s.b, s.g, s.seqlen and s.tiles are set.
+// The segment after s; false when the range is done.
+template <int TILE>
 __device__ __forceinline__ bool tree_next(const TreeParams& tp, TreeSeg& s) {
     s.x += s.t1 - s.t0;
     if (s.x >= s.x_end) return false;
@@ -162,7 +194,7 @@ __device__ __forceinline__ bool tree_next(const TreeParams& tp, TreeSeg& s) {
         do {
             if (++s.b == tp.d.B) return false;     // (the lengths changed under the kernel)
             s.seqlen = decode_seqlen(tp.d, s.b);
-            s.tiles = tree_tiles(s.seqlen);
+            s.tiles = tree_tiles<TILE>(s.seqlen);
         } while (s.tiles == 0);
     }
     s.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), s.x_end - s.x));
@@ -170,13 +202,14 @@ __device__ __forceinline__ bool tree_next(const TreeParams& tp, TreeSeg& s) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
+__global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const TreeParams tp) {
     grid_dep_release();   // the combine launch may be scheduled now
-    using L = TreeSmem<D>;
+    using L = TreeCfg<D>;
+    constexpr int kTile = L::kTile, kWarps = L::kThreads / 32;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ long long s_warp[kDtcThreads / 32], s_before;
+    __shared__ long long s_warp[kWarps], s_before;
     __shared__ int s_b;
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -187,10 +220,10 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // ---- this CTA's range of the line of tiles ----
-    const int per_thread = (p.B + kDtcThreads - 1) / kDtcThreads;
+    const int per_thread = (p.B + L::kThreads - 1) / L::kThreads;
     const int my_b = min(p.B, static_cast<int>(threadIdx.x) * per_thread), my_end = min(p.B, my_b + per_thread);
     long long mine = 0;
-    for (int b = my_b; b < my_end; ++b) mine += tree_tiles(decode_seqlen(p, b));
+    for (int b = my_b; b < my_end; ++b) mine += tree_tiles<kTile>(decode_seqlen(p, b));
     long long before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -202,17 +235,17 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
     __syncthreads();
     long long total = 0;
 #pragma unroll
-    for (int w = 0; w < kDtcThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_warp[w];
         total += s_warp[w];
     }
     total *= p.Hkv;
-    const long long per = max((total + tp.n_ranges - 1) / tp.n_ranges, static_cast<long long>(tp.min_tiles));
+    const long long per = max((total + tp.n_ranges - 1) / tp.n_ranges, 2ll);   // (a tile's softmax costs less than a partial)
     if (blockIdx.x == 0) {                        // for the combine
         long long t = before;
         for (int b = my_b; b < my_end; ++b) {
             tp.tiles_before[b] = t;
-            t += tree_tiles(decode_seqlen(p, b));
+            t += tree_tiles<kTile>(decode_seqlen(p, b));
         }
         if (threadIdx.x == 0) tp.tiles_before[p.B] = per;
     }
@@ -222,7 +255,7 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
     if (first.x >= first.x_end) return;           // uniform: nothing left for this range
     if (before * p.Hkv <= first.x && first.x < (before + mine) * p.Hkv) {
         int b = my_b;
-        for (int t; first.x >= (before + (t = tree_tiles(decode_seqlen(p, b)))) * p.Hkv; ++b) before += t;
+        for (int t; first.x >= (before + (t = tree_tiles<kTile>(decode_seqlen(p, b)))) * p.Hkv; ++b) before += t;
         s_b = b;
         s_before = before;
     }
@@ -231,28 +264,26 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
     const int R = min(128, RG - mblk * 128);       // of this block
     const int box = min(128, RG);                  // rows TMA loads (past the block's: another head's, or 0)
 
-    const uint32_t sQ = base + L::kQOff;
+    const uint32_t sQ = base;
     const uint32_t sKV = base + L::kKVOff;
     const uint32_t bar0 = base + L::kBarOff;
-    const uint32_t bar_q_full = bar0;
-    auto bar_full = [&](int s) { return bar0 + 8u * (1 + s); };
-    auto bar_empty = [&](int s) { return bar0 + 8u * (1 + L::kStages + s); };
-    auto bar_s_full = [&](int i) { return bar0 + 8u * (1 + 2 * L::kStages + i); };
-    auto bar_p_full = [&](int i) { return bar0 + 8u * (3 + 2 * L::kStages + i); };
-    const uint32_t bar_o_ready = bar0 + 8u * (5 + 2 * L::kStages);
-    const uint32_t bar_o_done = bar_o_ready + 8u;
-    const uint32_t bar_drain = bar_o_ready + 16u;
-    const uint32_t bar_q_empty = bar_o_ready + 24u;
+    const uint32_t bar_q_full = bar0, bar_q_empty = bar0 + 8u;
+    auto bar_full = [&](int s) { return bar0 + 8u * (2 + s); };
+    auto bar_empty = [&](int s) { return bar0 + 8u * (2 + L::kStages + s); };
+    constexpr uint32_t kB2 = 2 + 2 * L::kStages;
+    auto bar_s_full = [&](int i) { return bar0 + 8u * (kB2 + i); };
+    auto bar_p_full = [&](int i) { return bar0 + 8u * (kB2 + 2 + i); };
+    const uint32_t bar_drain = bar0 + 8u * (kB2 + 4);
     uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
     // segment n whose tree rows lost non-finite elements: n + 1 in entry n % 2 (the MMA warp is
     // at most one segment ahead of the epilogue)
     volatile int* v_patched = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
-    // (debug builds) the ring position the producer put in each entry, checked by the MMA warp
+    // (debug builds) the item the producer put in each ring entry, checked by the MMA warp
     volatile int* ring_tag = reinterpret_cast<volatile int*>(smem + L::kTagOff);
 
     if (threadIdx.x == 0) {
-        mbar_init(bar_q_full, 1);
+        mbar_init(bar_q_full, L::kQTmem ? 128 : 1);
         mbar_init(bar_q_empty, 1);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_full(s), 1);
@@ -263,23 +294,21 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
             mbar_init(bar_p_full(i), 128);
             v_patched[i] = 0;
         }
-        mbar_init(bar_o_ready, 1);
-        mbar_init(bar_o_done, 1);
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     // query rows past the box are not loaded: make them zero (finite) for the MMA
-    if (box < 128) {
+    if (!L::kQTmem && box < 128) {
         const int pad = (128 - box) * 128;
         for (int kb = 0; kb < L::kKB; ++kb) {
-            uint8_t* blk = smem + L::kQOff + kb * L::kQBlockBytes + box * 128;
-            for (int i = threadIdx.x * 16; i < pad; i += kDtcThreads * 16)
+            uint8_t* blk = smem + kb * L::kQBlockBytes + box * 128;
+            for (int i = threadIdx.x * 16; i < pad; i += L::kThreads * 16)
                 *reinterpret_cast<uint4*>(blk + i) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
     }
-    if (warp == kDtcMmaWarp) {
+    if (warp == L::kMmaWarp) {
         tmem_alloc(smem_u32(tmem_base_ptr), L::kTmemCols);
         tmem_relinquish();
     }
@@ -287,13 +316,13 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_base_ptr;
-    const uint32_t tS[2] = {tmem, tmem + 64u};    // S buffers (P over the first 32 columns)
-    const uint32_t tO = tmem + 128u;               // O
+    auto tS = [&](int buf) { return tmem + static_cast<uint32_t>(kTile * buf); };
+    const uint32_t tO = tmem + L::kTmemO;
 
     first.n = 0;
     first.b = s_b;
     first.seqlen = decode_seqlen(p, first.b);
-    first.tiles = tree_tiles(first.seqlen);
+    first.tiles = tree_tiles<kTile>(first.seqlen);
     {
         const long long in_b = first.x - s_before * p.Hkv;
         first.g = static_cast<int>(in_b / first.tiles);
@@ -301,178 +330,214 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
         first.t1 = static_cast<int>(min(static_cast<long long>(first.tiles), first.t0 + (first.x_end - first.x)));
     }
 
-    // The ring's items are numbered through the whole range; a segment's, from 2 x its tiles before:
-    // K_0 K_1 V_0 K_2 V_1 ...
-    auto slot_of = [&](int t) { return t % L::kStages; };
-    auto par_of = [&](int t) { return static_cast<uint32_t>(t / L::kStages) & 1u; };
+    // The ring's items, K and V tiles, are numbered through the whole range: segment after
+    // segment, in each K_0 K_1 V_0 K_2 V_1 ... (ring_order.cuh), which is also the order in
+    // which the MMAs use them.  Tile jj of the range (counted through all segments) has S
+    // buffer jj % 2.
+    struct RingPos {
+        int e = 0, item = 0;
+        uint32_t par = 0;
+        __device__ __forceinline__ void next() {
+            ++item;
+            if (++e == L::kStages) {
+                e = 0;
+                par ^= 1u;
+            }
+        }
+    };
 
-    if (warp == kDtcProducerWarp) {
-        // ================= TMA producer =================
+    if (warp == L::kProducerWarp) {
+        // ================= TMA producer (lane 0 issues; the warp looks the pages up) =================
         if (lane == 0) {
             tma_prefetch_desc(&tm_q);
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
-            int issued = 0;
-            bool ok = true;
-            TreeSeg s = first;
-            do {
-                const int n_tiles = s.t1 - s.t0, item0 = issued;
-                // (its last Q K^T is two tiles before the end of the segment before)
+        }
+        RingPos at;
+        bool ok = true;
+        TreeSeg s = first;
+        do {
+            const int n_tiles = s.t1 - s.t0;
+            if (!L::kQTmem) {
+                // (the last Q K^T of a segment is issued two tiles before its end)
                 ok = mbar_wait(bar_q_empty, (s.n & 1) ^ 1u, abort_flag, &g_attn_err, kDevErrTimeout);
                 if (!ok) break;
-                const size_t row0 = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.g) * p.G) * p.Lq + mblk * 128;
-                mbar_arrive_expect_tx(bar_q_full, static_cast<uint32_t>(L::kKB * box * 128));
-                for (int kb = 0; kb < L::kKB; ++kb)
-                    tma_load_3d(sQ + kb * L::kQBlockBytes, &tm_q, bar_q_full, kb * 64, static_cast<int>(row0), 0);
-                for (int i = 0; i < 2 * n_tiles; ++i) {
-                    const int t = item0 + i, e = slot_of(t);
-                    ok = mbar_wait(bar_empty(e), par_of(t) ^ 1u, abort_flag, &g_attn_err, kDevErrTimeout);
-                    if (!ok) break;
-                    bool is_v;
-                    int j;
-                    ring_tile<1>(i, n_tiles, is_v, j);
-                    const int key0 = (s.t0 + j) * kDtcBN;
-                    int row = key0, outer = s.b * p.Hkv + s.g;
-                    if (p.block_table != nullptr) {
-                        int page = __ldg(p.block_table + static_cast<size_t>(s.b) * p.max_pages + key0 / p.page_size);
-                        if (page < 0 || page >= p.n_pages) {
-                            atomicOr(&g_attn_err, kDevErrPage);
-                            page = 0;
-                        }
-                        row = key0 % p.page_size;
-                        outer = page * p.Hkv + s.g;
-                    }
-                    decode_check_tile(p, row, outer);
-                    ATTN_CHECK(j >= 0 && j < n_tiles && s.b < p.B && s.g < p.Hkv);
-                    if (ATTN_DEBUG_BOUNDS) ring_tag[e] = t;
-                    mbar_arrive_expect_tx(bar_full(e), L::kHalfBytes);
-                    const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-                    const uint32_t dst = sKV + e * L::kHalfBytes;
+                if (lane == 0) {
+                    const size_t row0 = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.g) * p.G) * p.Lq + mblk * 128;
+                    mbar_arrive_expect_tx(bar_q_full, static_cast<uint32_t>(L::kKB * box * 128));
                     for (int kb = 0; kb < L::kKB; ++kb)
-                        tma_load_3d(dst + kb * L::kHalfBlockBytes, map, bar_full(e), kb * 64, row, outer);
-                    issued = t + 1;
+                        tma_load_3d(sQ + kb * L::kQBlockBytes, &tm_q, bar_q_full, kb * 64, static_cast<int>(row0), 0);
                 }
-            } while (ok && tree_next(tp, s));
-            if (!ok) {
-                // unwinding after a timeout: let issued copies land first
-                for (int t = max(0, issued - L::kStages); t < issued; ++t) {
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(bar_full(slot_of(t)), par_of(t)) && global_timer_ns() - t0 < 100000000ull) {
+                __syncwarp();
+            }
+            // Pages of the segment's 64-row boxes, a window of 32 in the warp's lanes and the next one
+            // on its way: looked up box by box, they held the loads back (64 requests: 977 us for 688).
+            const int boxes_before = s.t0 * (kTile / 64), boxes_end = min(s.t1 * (kTile / 64), (s.seqlen + 63) / 64);
+            int window = boxes_before, here = 0, after = 0;
+            auto lookup = [&](int box0) {
+                const int i = box0 + lane;
+                if (p.block_table == nullptr || i >= boxes_end) return 0;
+                const int page = __ldg(p.block_table + static_cast<size_t>(s.b) * p.max_pages +
+                                       static_cast<int>(static_cast<long long>(i) * 64 / p.page_size));
+                if (page >= 0 && page < p.n_pages) return page;
+                atomicOr(&g_attn_err, kDevErrPage);
+                return 0;
+            };
+            here = lookup(window);
+            after = lookup(window + 32);
+            for (int i = 0; i < 2 * n_tiles; ++i) {
+                bool is_v;
+                int j;
+                ring_tile<1>(i, n_tiles, is_v, j);
+                ATTN_CHECK(j >= 0 && j < n_tiles && s.b < p.B && s.g < p.Hkv);
+                const int box0 = boxes_before + j * (kTile / 64);
+                const int boxes = min(kTile / 64, boxes_end - box0);
+                if (is_v && box0 >= window + 32) {             // (K is at most two tiles ahead of V)
+                    window += 32;
+                    here = after;
+                    after = lookup(window + 32);
+                }
+                ok = mbar_wait(bar_empty(at.e), at.par ^ 1u, abort_flag, &g_attn_err, kDevErrTimeout);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (ATTN_DEBUG_BOUNDS) ring_tag[at.e] = at.item;
+                    mbar_arrive_expect_tx(bar_full(at.e), static_cast<uint32_t>(boxes * 64 * D * 2));
+                }
+                const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+#pragma unroll
+                for (int h = 0; h < kTile / 64; ++h) {
+                    const int k = box0 + h - window;
+                    const int page = __shfl_sync(0xffffffffu, k < 32 ? here : after, k & 31);
+                    if (lane == 0 && h < boxes) {
+                        const int key = (box0 + h) * 64;
+                        int row = key, outer = s.b * p.Hkv + s.g;
+                        if (p.block_table != nullptr) {
+                            row = key % p.page_size;
+                            outer = page * p.Hkv + s.g;
+                        }
+                        decode_check_tile(p, row, outer);
+                        const uint32_t dst = sKV + at.e * L::kTileBytes + h * 64 * 128;
+                        for (int kb = 0; kb < L::kKB; ++kb)
+                            tma_load_3d(dst + kb * L::kBlockBytes, map, bar_full(at.e), kb * 64, row, outer);
                     }
                 }
+                at.next();
+            }
+        } while (ok && tree_next<kTile>(tp, s));
+        if (!ok && lane == 0) {
+            // unwinding after a timeout: let issued copies land first
+            for (int k = min(at.item, L::kStages); k > 0; --k) {
+                const int t = at.item - k;
                 const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(bar_q_full, s.n & 1) && global_timer_ns() - t0 < 100000000ull) {
+                while (!mbar_try_wait(bar_full(t % L::kStages), static_cast<uint32_t>(t / L::kStages) & 1u) &&
+                       global_timer_ns() - t0 < 100000000ull) {
                 }
+            }
+            const uint64_t t0 = global_timer_ns();
+            while (!L::kQTmem && !mbar_try_wait(bar_q_full, s.n & 1) && global_timer_ns() - t0 < 100000000ull) {
             }
         }
         __syncwarp();
-    } else if (warp == kDtcMmaWarp) {
+    } else if (warp == L::kMmaWarp) {
         // ================= MMA issuer (lane 0 issues; the warp mends V rows) =================
-        constexpr uint32_t kIdescQK = umma_idesc_bf16_f32(128, kDtcBN, false);
+        constexpr uint32_t kIdescQK = umma_idesc_bf16_f32(128, kTile, false);
         constexpr uint32_t kIdescPV = umma_idesc_bf16_f32(128, D, true);
         const uint64_t dQ = umma_sdesc_sw128(sQ, 16, 1024);
         const uint64_t dK0 = umma_sdesc_sw128(sKV, 16, 1024);
-        const uint64_t dV0 = umma_sdesc_sw128(sKV, L::kHalfBlockBytes, 1024);
-        constexpr uint64_t kSlotStep = L::kHalfBytes >> 4;
-        auto wait_item = [&](int it) {
-            const bool got = mbar_wait(bar_full(slot_of(it)), par_of(it), abort_flag, &g_attn_err, kDevErrTimeout);
-            if (got) ATTN_CHECK(ring_tag[slot_of(it)] == it);   // (debug builds) the entry holds that item
+        const uint64_t dV0 = umma_sdesc_sw128(sKV, L::kBlockBytes, 1024);
+        constexpr uint64_t kEntryStep = L::kTileBytes >> 4;
+        RingPos at;
+        // Every step is the warp's, with one thread issuing, and every wait's outcome the warp's vote
+        const uint32_t leader = lane == 0 ? 1u : 0u;
+        auto wait_bar = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_attn_err, kDevErrTimeout)) != 0;
+        };
+        auto wait_item = [&]() {
+            const bool got = wait_bar(bar_full(at.e), at.par);
+            if (got) ATTN_CHECK(ring_tag[at.e] == at.item);   // (debug builds) the entry holds that item
             return got;
         };
         bool ok = true;
         int tile0 = 0;                             // tiles of the segments before
         TreeSeg s = first;
         do {
-            const int n_tiles = s.t1 - s.t0, item0 = 2 * tile0;
-            // S(j) = Q K_j^T into the buffer of tile tile0 + j (N = 64 cache rows)
+            const int n_tiles = s.t1 - s.t0;
+            // S(j) = Q K_j^T (N = kTile cache rows)
             auto qk = [&](int j) {
-                const int it = item0 + ring_pos_k<1>(j), buf = (tile0 + j) & 1;
-                if (!wait_item(it)) return false;
+                if (!wait_item()) return false;
                 tc_fence_after_sync();
-                if (lane == 0) {
-                    const uint64_t b0 = dK0 + static_cast<uint64_t>(slot_of(it)) * kSlotStep;
+                const uint32_t d = tS((tile0 + j) & 1);
+                const uint64_t b0 = dK0 + static_cast<uint64_t>(at.e) * kEntryStep;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t koff = static_cast<uint64_t>(((kk >> 2) * L::kBlockBytes + (kk & 3) * 32) >> 4);
+                    if constexpr (L::kQTmem) {
+                        umma_ts_by(leader, d, tmem + L::kTmemQ + kk * 8, b0 + koff, kIdescQK, kk > 0 ? 1u : 0u);
+                    } else {
                         const uint64_t qoff = static_cast<uint64_t>(((kk >> 2) * L::kQBlockBytes + (kk & 3) * 32) >> 4);
-                        const uint64_t koff = static_cast<uint64_t>(((kk >> 2) * L::kHalfBlockBytes + (kk & 3) * 32) >> 4);
-                        umma_ss(tS[buf], dQ + qoff, b0 + koff, kIdescQK, kk > 0 ? 1u : 0u);
+                        umma_ss_by(leader, d, dQ + qoff, b0 + koff, kIdescQK, kk > 0 ? 1u : 0u);
                     }
-                    umma_commit(bar_empty(slot_of(it)));
-                    umma_commit(bar_s_full(buf));
-                    if (j + 1 == n_tiles) umma_commit(bar_q_empty);
                 }
-                __syncwarp();
+                umma_commit_by(leader, bar_s_full((tile0 + j) & 1));
+                umma_commit_by(leader, bar_empty(at.e));
+                if (!L::kQTmem && j + 1 == n_tiles) umma_commit_by(leader, bar_q_empty);
+                at.next();
                 return true;
             };
             const int ctx = s.seqlen - tree_len(tp, s.b);
-            const int k_end = min(s.t1 * kDtcBN, s.seqlen);
-            ok = mbar_wait(bar_q_full, s.n & 1, abort_flag, &g_attn_err, kDevErrTimeout);
+            const int k_end = min(s.t1 * kTile, s.seqlen);
+            ok = wait_bar(bar_q_full, s.n & 1);
             if (ok) ok = qk(0);
             if (ok && n_tiles > 1) ok = qk(1);
             for (int j = 0; j < n_tiles && ok; ++j) {
-                const int buf = (tile0 + j) & 1;
-                const int itv = item0 + ring_pos_v<1>(j, n_tiles);
-                ok = wait_item(itv);
+                const int jj = tile0 + j, buf = jj & 1;
+                ok = wait_item();
                 if (!ok) break;
-                const int key0 = (s.t0 + j) * kDtcBN;
-                const int valid = k_end - key0;
-                uint8_t* ent = smem + L::kKVOff + slot_of(itv) * L::kHalfBytes;
-                bool wrote = false;
-                // non-finite elements of tree rows: zero, and noted for the epilogue
-                const int tree_lo = max(0, ctx - key0), tree_hi = min(kDtcBN, valid);
-                if (tree_lo < tree_hi) {
+                const int key0 = (s.t0 + j) * kTile;
+                const int valid = min(kTile, k_end - key0);
+                // rows of the tree, or past the last one: seldom
+                if (key0 + kTile > ctx || valid < kTile) {
+                    uint8_t* ent = smem + L::kKVOff + at.e * L::kTileBytes;
+                    // non-finite elements of tree rows: zero, and noted for the epilogue
+                    const int tree_lo = max(0, ctx - key0);
                     for (int kb = 0; kb < L::kKB; ++kb) {
-                        uint8_t* blk = ent + kb * L::kHalfBlockBytes;
+                        uint8_t* blk = ent + kb * L::kBlockBytes;
 #pragma unroll 4
-                        for (int i = tree_lo * 128 + lane * 16; i < tree_hi * 128; i += 32 * 16) {
+                        for (int i = tree_lo * 128 + lane * 16; i < valid * 128; i += 32 * 16) {
                             uint4 x = *reinterpret_cast<const uint4*>(blk + i);
                             const uint32_t bad[4] = {nonfinite_bf16x2(x.x), nonfinite_bf16x2(x.y), nonfinite_bf16x2(x.z),
                                                      nonfinite_bf16x2(x.w)};
                             if (bad[0] | bad[1] | bad[2] | bad[3]) {
                                 x = make_uint4(x.x & ~bad[0], x.y & ~bad[1], x.z & ~bad[2], x.w & ~bad[3]);
                                 *reinterpret_cast<uint4*>(blk + i) = x;
-                                wrote = true;
                                 v_patched[s.n & 1] = s.n + 1;
                             }
                         }
-                    }
-                }
-                // V rows past the last row: zero (P is 0 there, but 0 * NaN is NaN)
-                if (valid < kDtcBN) {
-                    for (int kb = 0; kb < L::kKB; ++kb) {
-                        uint8_t* blk = ent + kb * L::kHalfBlockBytes + valid * 128;
-                        for (int i = lane * 16; i < (kDtcBN - valid) * 128; i += 32 * 16)
+                        // V rows past the last row: zero (P is 0 there, but 0 * NaN is NaN)
+                        for (int i = valid * 128 + lane * 16; i < L::kBlockBytes; i += 32 * 16)
                             *reinterpret_cast<uint4*>(blk + i) = make_uint4(0, 0, 0, 0);
                     }
-                    wrote = true;
-                }
-                if (__any_sync(0xffffffffu, wrote)) {
                     __threadfence_block();
                     fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                __syncwarp();
                 // P(j) is written, and, for the first tile, the epilogue before has read O
-                ok = mbar_wait(bar_p_full(buf), static_cast<uint32_t>((tile0 + j) >> 1) & 1u, abort_flag, &g_attn_err,
-                               kDevErrTimeout);
+                ok = wait_bar(bar_p_full(buf), static_cast<uint32_t>(jj >> 1) & 1u);
                 if (!ok) break;
-                __syncwarp();
                 tc_fence_after_sync();
-                if (lane == 0) {
-                    // O += P(j) V_j: 4 steps of 16 cache rows
-                    const uint64_t b0 = dV0 + static_cast<uint64_t>(slot_of(itv)) * kSlotStep;
+                // O += P(j) V_j: steps of 16 cache rows.  (A commit holds the tensor pipe up by about 100
+                // cycles: the entry's release is also what the softmax waits on for O.)
+                const uint64_t b0 = dV0 + static_cast<uint64_t>(at.e) * kEntryStep;
 #pragma unroll
-                    for (int kk = 0; kk < kDtcBN / 16; ++kk)
-                        umma_ts(tO, tS[buf] + kk * 8, b0 + static_cast<uint64_t>((kk * 2048) >> 4), kIdescPV,
-                                (j > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(bar_o_ready);
-                    if (j + 1 == n_tiles) umma_commit(bar_o_done);
-                    umma_commit(bar_empty(slot_of(itv)));
-                }
-                __syncwarp();
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    umma_ts_by(leader, tO, tS(buf) + kk * 8, b0 + static_cast<uint64_t>((kk * 2048) >> 4), kIdescPV,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                umma_commit_by(leader, bar_empty(at.e));
+                at.next();
                 if (j + 2 < n_tiles) ok = qk(j + 2);
             }
             tile0 += n_tiles;
-        } while (ok && tree_next(tp, s));
+        } while (ok && tree_next<kTile>(tp, s));
         if (lane == 0) {
             // Drain: no MMA may still be running when TMEM is released.
             umma_commit(bar_drain);
@@ -498,12 +563,36 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
         TreeSeg s = first;
         do {
             const int n_tiles = s.t1 - s.t0;
+            const size_t row = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.g) * p.G) * p.Lq + mblk * 128 +
+                               (r < R ? r : 0);
+            if constexpr (L::kQTmem) {
+                // Q's row to TMEM (the last S of the segment before is complete, so its Q is used)
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
+#pragma unroll
+                for (int c = 0; c < D / 64; c += 2) {
+                    uint4 x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = r < R ? __ldg(src + c * 8 + i) : make_uint4(0, 0, 0, 0);
+                    tmem_st_32x32b_x32(tmem + L::kTmemQ + lane_off + c * 32, reinterpret_cast<const uint32_t*>(x));
+                    tmem_st_32x32b_x32(tmem + L::kTmemQ + lane_off + c * 32 + 32, reinterpret_cast<const uint32_t*>(x) + 32);
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(bar_q_full);
+            }
             const int n_tree = tree_len(tp, s.b);
             const int ctx = s.seqlen - n_tree;     // rows every node sees (negative: the tree's first rows are not cached)
-            const int k_end = min(s.t1 * kDtcBN, s.seqlen);
+            const int k_end = min(s.t1 * kTile, s.seqlen);
             const bool live = r < R && node < n_tree;
             const uint32_t* words = tp.mask + static_cast<size_t>(s.b) * tp.mask_batch + static_cast<size_t>(node) * tp.W;
             const int free_end = min(ctx, k_end);  // rows below it need no mask
+            // O += P V of tile j is done: V_j's ring entry is released.  (The entry cannot be released
+            // again before this wait: what comes into it next is used after P of a later tile.)
+            auto wait_o = [&](int j) {
+                const int item = 2 * tile0 + ring_pos_v<1>(j, n_tiles);
+                return mbar_wait(bar_empty(item % L::kStages), static_cast<uint32_t>(item / L::kStages) & 1u, abort_flag,
+                                 &g_attn_err, kDevErrTimeout);
+            };
             // l_run: row sum of P as rounded to bf16 (normalises O); l_exact: of the
             // unrounded exponentials (for the log-sum-exp)
             float m_run = -INFINITY, l_run = 0.0f, l_exact = 0.0f;
@@ -518,16 +607,15 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
                     mbar_arrive(bar_p_full(buf));
                     continue;
                 }
-                const uint32_t tSr = tS[buf] + lane_off;
-                const int key0 = (s.t0 + j) * kDtcBN;
-                const bool masked = key0 + kDtcBN > free_end;
-                // the tile's 64 scores of this row, read from TMEM once
-                uint32_t v[kDtcBN];
+                const uint32_t tSr = tS(buf) + lane_off;
+                const int key0 = (s.t0 + j) * kTile;
+                // the tile's scores of this row, read from TMEM once
+                uint32_t v[kTile];
                 tmem_ld_32x32b_x32(tSr, v);
                 tmem_ld_32x32b_x32(tSr + 32, v + 32);
                 tmem_wait_ld();
-                reg_fence<kDtcBN>(v);
-                if (masked) {
+                reg_fence<kTile>(v);
+                if (key0 + kTile > free_end) {
                     const uint64_t vis = tree_visible(words, tp.W, ctx, key0) & low_bits(k_end - key0);
                     const uint32_t vlo = static_cast<uint32_t>(vis), vhi = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
@@ -538,7 +626,7 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
                 }
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kDtcBN; i += 8) {
+                for (int i = 0; i < kTile; i += 8) {
                     mx0 = fmax3(mx0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                     mx1 = fmax3(mx1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                     mx2 = fmax3(mx2, __uint_as_float(v[i + 4]), __uint_as_float(v[i + 5]));
@@ -553,28 +641,27 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
                     l_exact *= factor;
                 }
                 if (j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
-                    // O must hold the tiles before: O += P V of the last one is the only one that can be in flight
-                    if (!mbar_wait(bar_o_ready, static_cast<uint32_t>(jj - 1) & 1u, abort_flag, &g_attn_err,
-                                   kDevErrTimeout)) {
+                    // O must hold the tiles before: the last one's O += P V is the only one that can be in flight
+                    if (!wait_o(j - 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const uint64_t f2 = f2_pack(factor, factor);
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(tOr + c, o);
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(tOr + c, o);
                         tmem_wait_ld();
-                        reg_fence<32>(o);
+                        reg_fence<16>(o);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             float a0, a1;
                             f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2), a0, a1);
                             o[i] = __float_as_uint(a0);
                             o[i + 1] = __float_as_uint(a1);
                         }
-                        tmem_st_32x32b_x32(tOr + c, o);
+                        tmem_st_32x32b_x16(tOr + c, o);
                     }
                     tmem_wait_st();
                 }
@@ -583,7 +670,7 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
                 const uint64_t negm2 = f2_pack(-m_sub, -m_sub);
                 uint64_t acc_r = 0ull, acc_e = 0ull;
 #pragma unroll
-                for (int c = 0; c < kDtcBN; c += 32) {
+                for (int c = 0; c < kTile; c += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -609,7 +696,7 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
             }
             if (!ok) break;
             // ---- the segment's O / l and log-sum-exp per row: the result, or a partial (fp32, log2) ----
-            ok = mbar_wait(bar_o_done, s.n & 1, abort_flag, &g_attn_err, kDevErrTimeout);
+            ok = wait_o(n_tiles - 1);
             if (!ok) break;
             tc_fence_after_sync();
             if (!idle_warp) {
@@ -619,161 +706,219 @@ __global__ void __launch_bounds__(kDtcThreads, DecodeTcSmem<D>::kCtasPerSm)
                 const bool seen = live && !(l_exact == 0.0f);
                 const float inv_l = seen ? 1.0f / l_run : 0.0f;
                 const float lse2 = seen ? m_run + __log2f(l_exact) : -INFINITY;
-                const size_t row = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.g) * p.G) * p.Lq + mblk * 128 +
-                                   (row_valid ? r : 0);
                 const size_t prow = tree_part(tp, range, mblk, s.n == 0 ? 0 : 1, row_valid ? r : 0);
                 ATTN_CHECK(row < static_cast<size_t>(p.B) * p.Hq * p.Lq);
                 ATTN_CHECK(whole || prow < static_cast<size_t>(tp.n_ranges) * tp.n_mblk * 2 * box);
-                // (seen by this row's node, and not finite)
-                const bool add = seen && v_patched[s.n & 1] == s.n + 1;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(tOr + c, o);
                     tmem_wait_ld();
                     reg_fence<32>(o);
+                    float x[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = seen ? __float_as_uint(__uint_as_float(o[i]) * inv_l) : 0u;
+                    for (int k = 0; k < 32; ++k) x[k] = seen ? __uint_as_float(o[k]) * inv_l : 0.0f;
                     if (row_valid && whole) {
                         __nv_bfloat16* dst = tp.out + row * D + c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            float x[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[i + k]);
-                            *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-                        }
+                        for (int k = 0; k < 32; k += 8)
+                            *reinterpret_cast<uint4*>(dst + k) =
+                                make_uint4(pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]),
+                                           pack_bf16x2(x[k + 4], x[k + 5]), pack_bf16x2(x[k + 6], x[k + 7]));
                     } else if (row_valid) {
                         float* dst = p.o_part + prow * D + c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                     }
                 }
-                if (row_valid && whole) {
-                    if (tp.lse != nullptr) tp.lse[row] = lse2 * kLn2;
-                    if (add) tree_add_nonfinite(tp, s.b, s.g, words, ctx, 0, k_end, D, tp.out + row * D);
-                } else if (row_valid) {
-                    p.lse_part[prow] = lse2;
-                    if (add) tree_add_nonfinite(tp, s.b, s.g, words, ctx, s.t0 * kDtcBN, k_end, D, p.o_part + prow * D);
+                // elements that the node sees and that are not finite
+                if (seen && v_patched[s.n & 1] == s.n + 1) {
+                    if (whole)
+                        tree_add_nonfinite(tp, s.b, s.g, words, ctx, 0, k_end, D, tp.out + row * D);
+                    else
+                        tree_add_nonfinite(tp, s.b, s.g, words, ctx, s.t0 * kTile, k_end, D, p.o_part + prow * D);
+                }
+                if (row_valid) {
+                    if (!whole)
+                        p.lse_part[prow] = lse2;
+                    else if (tp.lse != nullptr)
+                        tp.lse[row] = lse2 * kLn2;
                 }
             }
             // O is read: the arrival on P of the next segment's first tile lets it be written
             tc_fence_before_sync();
             tile0 += n_tiles;
-        } while (tree_next(tp, s));
+        } while (tree_next<kTile>(tp, s));
     }
 
     // ---- teardown ----
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kDtcMmaWarp) {
+    if (warp == L::kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, L::kTmemCols);
     }
 }
 
-// out = sum_k 2^(lse_k - lse) O_k, lse = log2 sum_k 2^lse_k over the partials of a (sequence,
-// KV head) pair that lies in several ranges; rows of sequences without rows get 0 and -inf;
-// the rows of other pairs are there already.  WPR warps per row (4: one row per CTA, for
-// pairs over many ranges), D / 32 columns per lane, kInFlight partials loaded at a time.
-template <int D, int WPR>
-__global__ void __launch_bounds__(128) attn_tree_combine_kernel(const TreeParams tp) {
-    grid_dep_wait();   // launched as a programmatic dependent of attn_tree_kernel
-    constexpr int kPer = D / 32;
-    constexpr int kInFlight = 8;
-    const DecodeParams& p = tp.d;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * (4 / WPR) + warp / WPR;
-    const int sub = warp % WPR;
-    if (row >= p.B * p.Hq * p.Lq) return;          // (uniform over a CTA when WPR = 4)
-    const int RG = p.G * p.Lq;
-    const int pair = row / RG, rr = row - pair * RG;
-    const int b = pair / p.Hkv, g = pair - b * p.Hkv;
-    const int mblk = rr / 128, r = rr % 128;
-    const int tiles = tree_tiles(decode_seqlen(p, b));
-    const long long per = tp.tiles_before[p.B];
-    const long long start = tp.tiles_before[b] * p.Hkv + static_cast<long long>(g) * tiles;
-    long long r0 = 0;
-    int n = 0;                                     // partials
+// Where the partials of a (sequence, KV head) pair lie.
+struct TreeParts {
+    long long start, per, r0;      // the pair's first tile in the line; tiles a range; first range
+    int n;                         // partials; 0: the sequence has no rows, 1: the result is written
+};
+
+template <int TILE>
+__device__ __forceinline__ TreeParts tree_parts(const TreeParams& tp, int b, int g) {
+    TreeParts q;
+    const int tiles = tree_tiles<TILE>(decode_seqlen(tp.d, b));
+    q.per = tp.tiles_before[tp.d.B];
+    q.start = tp.tiles_before[b] * tp.d.Hkv + static_cast<long long>(g) * tiles;
+    q.r0 = 0;
+    q.n = 0;
     if (tiles > 0) {
-        r0 = start / per;
-        n = static_cast<int>((start + tiles - 1) / per - r0) + 1;
-        if (n == 1) return;
+        q.r0 = q.start / q.per;
+        q.n = static_cast<int>((q.start + tiles - 1) / q.per - q.r0) + 1;
     }
-    auto part = [&](int k) { return tree_part(tp, r0 + k, mblk, k == 0 && start != r0 * per ? 1 : 0, r); };
-    float M = -INFINITY, Lsum = 0.0f, acc[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-    for (int k0 = sub; k0 < n; k0 += WPR * kInFlight) {
-        float ls[kInFlight], ov[kInFlight][kPer];
-#pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            const int k = k0 + u * WPR;
-            ls[u] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) ov[u][i] = 0.0f;
-            if (k < n) {
-                const size_t at = part(k);
-                ls[u] = p.lse_part[at];
-                const float* src = p.o_part + at * D + lane * kPer;
-#pragma unroll
-                for (int i = 0; i < kPer; i += 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(src + i);
-                    ov[u][i] = v.x;
-                    ov[u][i + 1] = v.y;
-                }
-            }
-        }
+    return q;
+}
+
+__device__ __forceinline__ size_t tree_part_row(const TreeParams& tp, const TreeParts& q, int k, int mblk, int r) {
+    return tree_part(tp, q.r0 + k, mblk, k == 0 && q.start != q.r0 * q.per ? 1 : 0, r);
+}
+
+// Running maximum, sum and O of one row's partials; kPer columns a lane.
+template <int kPer>
+struct TreeMerge {
+    float M = -INFINITY, sum = 0.0f, acc[kPer] = {};
+
+    template <int N>
+    __device__ __forceinline__ void add(const float (&ls)[N], const float (&ov)[N][kPer]) {
         float top = M;
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, ls[u]);
-        const float f = M == -INFINITY ? 0.0f : ex2_approx(M - top);
+        for (int u = 0; u < N; ++u) top = fmaxf(top, ls[u]);
+        const float f = M == -INFINITY ? 1.0f : ex2_approx(M - top);   // (M = -inf: sum is 0, or NaN to stay)
         M = top;
-        Lsum *= f;
+        sum *= f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) acc[i] *= f;
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
+        for (int u = 0; u < N; ++u) {
             const float w = ls[u] == -INFINITY ? 0.0f : ex2_approx(ls[u] - M);
-            Lsum += w;
+            sum += w;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) acc[i] = w == 0.0f ? acc[i] : fmaf(w, ov[u][i], acc[i]);
         }
     }
-    if constexpr (WPR > 1) {
-        __shared__ float red_m[WPR], red_l[WPR], red_acc[WPR][D];
+    // a sum of 0: the row saw nothing; NaN: a score was
+    __device__ __forceinline__ void store(const TreeParams& tp, size_t row, int D, int lane) const {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        __nv_bfloat16* o = tp.out + row * D + lane * kPer;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) red_acc[sub][lane * kPer + i] = acc[i];
-        if (lane == 0) {
-            red_m[sub] = M;
-            red_l[sub] = Lsum;
-        }
-        __syncthreads();
-        if (sub != 0) return;
-        float top = M;
-#pragma unroll
-        for (int w = 1; w < WPR; ++w) top = fmaxf(top, red_m[w]);
-        Lsum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WPR; ++w) {
-            // (a warp that saw only NaN has M = -inf and a NaN sum)
-            const float f = red_m[w] == -INFINITY ? 1.0f : ex2_approx(red_m[w] - top);
-            Lsum += red_l[w] * f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] = f == 0.0f ? acc[i] : fmaf(f, red_acc[w][lane * kPer + i], acc[i]);
-        }
-        M = top;
+        for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(o + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+        if (tp.lse != nullptr && lane == 0) tp.lse[row] = sum == 0.0f ? -INFINITY : (M + __log2f(sum)) * kLn2;
     }
-    // a sum of 0: no row was seen; NaN: a score was
-    const float inv = Lsum == 0.0f ? 0.0f : 1.0f / Lsum;
-    __nv_bfloat16* o = tp.out + static_cast<size_t>(row) * D + lane * kPer;
+};
+
+template <int kPer>
+__device__ __forceinline__ void load_cols(const float* src, float (&x)[kPer]) {
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(o + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-    if (tp.lse != nullptr && lane == 0) tp.lse[row] = Lsum == 0.0f ? -INFINITY : (M + __log2f(Lsum)) * kLn2;
+    for (int i = 0; i < kPer; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(src + i);
+        x[i] = v.x;
+        x[i + 1] = v.y;
+    }
+}
+
+// out = sum_k 2^(lse_k - lse) O_k, lse = log2 sum_k 2^lse_k over the partials of a (sequence,
+// KV head) pair that lies in several ranges; rows of sequences without rows get 0 and -inf;
+// the rows of other pairs are there already.  A CTA takes 32 rows of a pair's query block, a
+// warp eight of them, kRows at a time and two partials of each (a pair has few).
+constexpr int kTreeCombineRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(128) attn_tree_combine_kernel(const TreeParams tp) {
+    grid_dep_wait();   // launched as a programmatic dependent of attn_tree_kernel
+    constexpr int kPer = D / 32, kRows = D == 256 ? 2 : 4;
+    const DecodeParams& p = tp.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int RG = p.G * p.Lq;
+    const int slices = (RG + kTreeCombineRows - 1) / kTreeCombineRows;      // (128 is a multiple of their rows)
+    const int pair = blockIdx.x / slices, rr0 = (blockIdx.x - pair * slices) * kTreeCombineRows + warp * 8;
+    const int b = pair / p.Hkv, g = pair - b * p.Hkv;
+    const TreeParts q = tree_parts<TreeCfg<D>::kTile>(tp, b, g);
+    if (q.n == 1) return;
+    const size_t row0 = static_cast<size_t>(pair) * RG;
+    for (int u0 = 0; u0 < 8; u0 += kRows) {
+        TreeMerge<kPer> m[kRows];
+        for (int k0 = 0; k0 < q.n; k0 += 2) {
+            float ls[kRows][2], ov[kRows][2][kPer];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int rr = min(rr0 + u0 + u, RG - 1);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // (past the last partial: it again, with weight 0)
+                    const size_t at = tree_part_row(tp, q, min(k0 + k, q.n - 1), rr / 128, rr % 128);
+                    ls[u][k] = k0 + k < q.n ? p.lse_part[at] : -INFINITY;
+                    load_cols<kPer>(p.o_part + at * D + lane * kPer, ov[u][k]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) m[u].add(ls[u], ov[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (rr0 + u0 + u < RG) m[u].store(tp, row0 + rr0 + u0 + u, D, lane);
+    }
+}
+
+// The same for pairs over many ranges: a CTA takes one row, its four warps every fourth
+// partial, eight at a time; their sums meet in shared memory.
+template <int D>
+__global__ void __launch_bounds__(128) attn_tree_combine_many_kernel(const TreeParams tp) {
+    grid_dep_wait();
+    constexpr int kPer = D / 32, kInFlight = 8;
+    const DecodeParams& p = tp.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x, RG = p.G * p.Lq;
+    const int pair = row / RG, rr = row - pair * RG;
+    const int b = pair / p.Hkv, g = pair - b * p.Hkv;
+    const TreeParts q = tree_parts<TreeCfg<D>::kTile>(tp, b, g);
+    if (q.n == 1) return;                          // uniform over the CTA
+    TreeMerge<kPer> m;
+    for (int k0 = warp; k0 < q.n; k0 += 4 * kInFlight) {
+        float ls[kInFlight], ov[kInFlight][kPer];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int k = k0 + 4 * u;
+            const size_t at = tree_part_row(tp, q, min(k, q.n - 1), rr / 128, rr % 128);
+            ls[u] = k < q.n ? p.lse_part[at] : -INFINITY;
+            load_cols<kPer>(p.o_part + at * D + lane * kPer, ov[u]);
+        }
+        m.add(ls, ov);
+    }
+    __shared__ float s_m[4], s_sum[4], s_acc[4][D];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = m.acc[i];
+    if (lane == 0) {
+        s_m[warp] = m.M;
+        s_sum[warp] = m.sum;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float top = m.M;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, s_m[w]);
+    TreeMerge<kPer> all;
+    all.M = top;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = s_m[w] == -INFINITY ? 1.0f : ex2_approx(s_m[w] - top);   // (-inf: sum 0, or NaN)
+        all.sum += s_sum[w] * f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) all.acc[i] = f == 0.0f ? all.acc[i] : fmaf(f, s_acc[w][lane * kPer + i], all.acc[i]);
+    }
+    all.store(tp, row, D, lane);
 }
 
 }  // namespace attn
