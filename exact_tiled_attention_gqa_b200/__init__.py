@@ -556,49 +556,19 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     return out, lse
 
 
-# The calls of a serving step are made at every layer or step, and on small batches the host
-# bounds them: their checks are one test per tensor on the way that passes, and the device and
-# stream contexts are entered only where they change something.
+# The calls of a serving step: checked, given results and workspaces, and made on the current
+# stream of the tensors' device by csrc/torch_calls.cpp.
 _HERE = contextlib.nullcontext()
 
 
-def _on(index: int, stream):
-    """Context of a call on CUDA device `index`: that device current and, where a stream is given, that
-    stream, so that the results and workspace the call makes belong to the stream that uses them."""
+def _on(stream, t):
+    """Context of a call on `stream`, so that the results and workspace the call makes belong to the stream that
+    uses them, and memory another stream still works on is not handed out for them."""
     if stream is None:
-        return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
-    if stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, but the call's tensors are on cuda:{index}")
+        return _HERE
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, but the call's tensors are on {t.device}")
     return torch.cuda.stream(stream)
-
-
-def _need(name: str, t, dtype: torch.dtype, ndim: int, ref: torch.Tensor) -> None:
-    """t is a contiguous dtype tensor of ndim dimensions on the CUDA device of ref."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda
-            and t.get_device() == ref.get_device() and t.is_contiguous()):
-        _check_tensor(name, t, dtype, ndim)
-        raise ValueError(f"{name} is on {t.device}, but the call's tensors are on {ref.device}")
-
-
-def _made(name: str, t, dtype: torch.dtype, shape, ref: torch.Tensor) -> torch.Tensor:
-    """A caller's result tensor, checked against the shape the call writes, or a new one beside ref."""
-    if t is None:
-        return ref.new_empty(shape, dtype=dtype)
-    _need(name, t, dtype, len(shape), ref)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
-
-
-def _at(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _c_int(name: str, x: int, low: int = 0) -> int:
-    x = int(x)
-    if not low <= x <= 0x7FFFFFFF:
-        raise ValueError(f"{name}={x} must lie in [{low}, 2^31 - 1]")
-    return x
 
 
 def pack_tree_mask(allowed: torch.Tensor) -> torch.Tensor:
@@ -613,27 +583,6 @@ def pack_tree_mask(allowed: torch.Tensor) -> torch.Tensor:
     return torch.where(words >= 1 << 31, words - (1 << 32), words).int()
 
 
-def _tree_args(q, seqlens, tree_mask, tree_lens, out, lse, want_lse: bool, workspace, need: int):
-    """Checks what decode_tree and decode_tree_paged share; (out, lse, workspace, its bytes)."""
-    B, Hq, T, _ = q.shape
-    if not isinstance(tree_mask, torch.Tensor) or tree_mask.dim() not in (2, 3):
-        raise ValueError("tree_mask must be a tensor [B,T,W] or [T,W]")
-    _need("tree_mask", tree_mask, torch.int32, tree_mask.dim(), q)
-    want = (T, -(-T // 32)) if tree_mask.dim() == 2 else (B, T, -(-T // 32))
-    if tree_mask.shape != want:
-        raise ValueError(f"tree_mask must have shape {want}, got {tuple(tree_mask.shape)}")
-    if tree_lens is not None:
-        _need("tree_lens", tree_lens, torch.int32, 1, q)
-        if tree_lens.shape[0] != B:
-            raise ValueError(f"tree_lens must have {B} entries")
-    out = torch.empty_like(q) if out is None else _made("out", out, torch.bfloat16, q.shape, q)
-    if lse is not None or want_lse:
-        lse = _made("lse", lse, torch.float32, (B, Hq, T), q)
-    if workspace is None:
-        return out, lse, q.new_empty(max(need, 1), dtype=torch.uint8), need
-    return out, lse, *_workspace(workspace, need, q.device)
-
-
 def decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, Lmax: int, D: int) -> int:
     return int(_native.lib().attn_decode_tree_workspace_size(B, Hq, Hkv, T, Lmax, D))
 
@@ -646,25 +595,9 @@ def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, s
     int32 [B]; the last tree_lens[b] (int32 [B]; T when None) of a sequence's cached rows are its tree's nodes.
     tree_mask int32 [B,T,W] or [T,W] (pack_tree_mask): node i sees every row before the tree and node j where bit
     j is set.  Nodes at or past tree_lens[b], and nodes that see no row: out = 0, lse = -inf."""
-    _check_tensor("q", q, torch.bfloat16, 4)
-    _need("k_cache", k_cache, torch.bfloat16, 4, q)
-    _need("v_cache", v_cache, torch.bfloat16, 4, q)
-    _need("seqlens", seqlens, torch.int32, 1, q)
-    B, Hq, T, D = q.shape
-    B2, Hkv, Lmax, D2 = k_cache.shape
-    if B2 != B or D2 != D or v_cache.shape != k_cache.shape or seqlens.shape[0] != B:
-        raise ValueError("shape mismatch between q, the caches and seqlens")
-    lib, index = _native.lib(), q.get_device()
-    with _on(index, stream):
-        need = lib.attn_decode_tree_workspace_size(B, Hq, Hkv, T, Lmax, D)
-        out, lse, workspace, ws_bytes = _tree_args(q, seqlens, tree_mask, tree_lens, out, lse, want_lse, workspace, need)
-        st = lib.attn_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
-                                  tree_mask.data_ptr(), tree_mask.dim() == 3, _at(tree_lens), out.data_ptr(), _at(lse),
-                                  B, Hq, Hkv, T, Lmax, D, 1.0 / math.sqrt(D) if scale is None else float(scale),
-                                  workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        _native.check(st, "attn_decode_tree")
-    return out, lse
+    with _on(stream, q):
+        return _native.calls().decode_tree(q, k_cache, v_cache, None, seqlens, tree_mask, tree_lens, scale, out, lse, want_lse,
+                                           workspace)
 
 
 def decode_tree_paged_workspace_size(B: int, Hq: int, Hkv: int, T: int, page_size: int, max_pages: int, D: int) -> int:
@@ -677,41 +610,11 @@ def decode_tree_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
                       lse: Optional[torch.Tensor] = None, want_lse: bool = True,
                       workspace: Optional[torch.Tensor] = None, stream=None):
     """decode_tree over a paged cache: pools [n_pages,Hkv,page_size,D], block_table int32 [B,max_pages]."""
-    _check_tensor("q", q, torch.bfloat16, 4)
-    _need("k_pages", k_pages, torch.bfloat16, 4, q)
-    _need("v_pages", v_pages, torch.bfloat16, 4, q)
-    _need("block_table", block_table, torch.int32, 2, q)
-    _need("seqlens", seqlens, torch.int32, 1, q)
-    B, Hq, T, D = q.shape
-    n_pages, Hkv, page_size, D2 = k_pages.shape
-    B2, max_pages = block_table.shape
-    if D2 != D or v_pages.shape != k_pages.shape or B2 != B or seqlens.shape[0] != B:
-        raise ValueError("shape mismatch between q, the page pools, block_table and seqlens")
-    lib, index = _native.lib(), q.get_device()
-    with _on(index, stream):
-        need = lib.attn_decode_tree_paged_workspace_size(B, Hq, Hkv, T, page_size, max_pages, D)
-        out, lse, workspace, ws_bytes = _tree_args(q, seqlens, tree_mask, tree_lens, out, lse, want_lse, workspace, need)
-        st = lib.attn_decode_tree_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-                                        seqlens.data_ptr(), tree_mask.data_ptr(), tree_mask.dim() == 3, _at(tree_lens),
-                                        out.data_ptr(), _at(lse), B, Hq, Hkv, T, n_pages, page_size, max_pages, D,
-                                        1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(),
-                                        ws_bytes, torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        _native.check(st, "attn_decode_tree_paged")
-    return out, lse
-
-
-def _check_pages(seqlens, lens, lens_name: str, block_table, free_pages, n_free) -> int:
-    """The arrays page_plan and page_release share; B."""
-    _check_tensor("seqlens", seqlens, torch.int32, 1)
-    _need(lens_name, lens, torch.int32, 1, seqlens)
-    _need("block_table", block_table, torch.int32, 2, seqlens)
-    _need("free_pages", free_pages, torch.int32, 1, seqlens)
-    _need("n_free", n_free, torch.int32, 1, seqlens)
-    B = seqlens.shape[0]
-    if lens.shape[0] != B or block_table.shape[0] != B or n_free.shape[0] != 1:
-        raise ValueError(f"shape mismatch between seqlens, {lens_name}, block_table and n_free")
-    return B
+    if block_table is None:
+        raise ValueError("block_table must be a tensor")
+    with _on(stream, q):
+        return _native.calls().decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens, scale, out, lse, want_lse,
+                                           workspace)
 
 
 def page_plan(seqlens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -724,21 +627,9 @@ def page_plan(seqlens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
     [1] valid entries, popped from the top, requests in order.  A request the pages do not reach for, or the table
     has no room for, is refused: status 1, length as it was, slots -1.  Returns (slots [B,L], out_seqlens [B],
     out_n_free [1], status [B]); out_seqlens may be seqlens and out_n_free n_free."""
-    B = _check_pages(seqlens, new_lens, "new_lens", block_table, free_pages, n_free)
-    L, page_size, n_pages = _c_int("L", L), _c_int("page_size", page_size), _c_int("n_pages", n_pages)
-    index = seqlens.get_device()
-    with _on(index, stream):
-        slots = _made("slots", slots, torch.int32, (B, L), seqlens)
-        out_seqlens = torch.empty_like(seqlens) if out_seqlens is None else _made("out_seqlens", out_seqlens, torch.int32, (B,), seqlens)
-        out_n_free = torch.empty_like(n_free) if out_n_free is None else _made("out_n_free", out_n_free, torch.int32, (1,), seqlens)
-        status = torch.empty_like(seqlens) if status is None else _made("status", status, torch.int32, (B,), seqlens)
-        st = _native.lib().attn_page_plan(seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
-                                          n_free.data_ptr(), slots.data_ptr(), out_seqlens.data_ptr(), out_n_free.data_ptr(),
-                                          status.data_ptr(), B, L, page_size, block_table.shape[1], free_pages.shape[0], n_pages,
-                                          torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        _native.check(st, "attn_page_plan")
-    return slots, out_seqlens, out_n_free, status
+    with _on(stream, seqlens):
+        return _native.calls().page_plan(seqlens, new_lens, block_table, free_pages, n_free, L, page_size, n_pages, slots, out_seqlens,
+                                         out_n_free, status)
 
 
 def page_release(seqlens: torch.Tensor, keep_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -746,34 +637,8 @@ def page_release(seqlens: torch.Tensor, keep_lens: torch.Tensor, block_table: to
                  stream=None):
     """The pages past each request's first keep_lens[b] of seqlens[b] rows go back on the stack free_pages (written
     from n_free on).  All int32 as in page_plan.  Returns out_n_free [1], which may be n_free."""
-    B = _check_pages(seqlens, keep_lens, "keep_lens", block_table, free_pages, n_free)
-    page_size, n_pages = _c_int("page_size", page_size), _c_int("n_pages", n_pages)
-    index = seqlens.get_device()
-    with _on(index, stream):
-        out_n_free = torch.empty_like(n_free) if out_n_free is None else _made("out_n_free", out_n_free, torch.int32, (1,), seqlens)
-        st = _native.lib().attn_page_release(seqlens.data_ptr(), keep_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
-                                             n_free.data_ptr(), out_n_free.data_ptr(), B, page_size, block_table.shape[1],
-                                             free_pages.shape[0], n_pages, torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        _native.check(st, "attn_page_release")
-    return out_n_free
-
-
-def _token_stride(name: str, t, ref) -> int:
-    """Elements from one token of t [B,L,H,D] to the next, heads dense."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 4 and t.is_cuda
-            and t.get_device() == ref.get_device()):
-        raise ValueError(f"{name} must be a 4-d bf16 CUDA tensor [B,L,H,D], on the device of q")
-    B, L, H, D = t.shape
-    sb, sl, sh, sd = t.stride()
-    if B * L == 0:
-        return H * D
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    step = sl if L > 1 else sb if B > 1 else H * D
-    if B > 1 and L > 1 and sb != L * step:
-        raise ValueError(f"the tokens of {name} must lie one stride apart (as in a part of one projection's output)")
-    return step
+    with _on(stream, seqlens):
+        return _native.calls().page_release(seqlens, keep_lens, block_table, free_pages, n_free, page_size, n_pages, out_n_free)
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -788,56 +653,11 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     k_scale / v_scale torch.float8_e4m3fn (scales fp32 [Hkv], read) or torch.int8 (fp16 [n,Hkv,rows,D/32], written).
     sections: pairs per axis (default: all on one axis); axis_order "blocks" or "cycle" (axes taken in turn);
     pairs "half" (i, i + rot / 2) or "adjacent" (2i, 2i + 1).  Returns the turned q as [B,Hq,L,D] bf16."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    q_step, k_step, v_step = _token_stride("q", q, q), _token_stride("k", k, q), _token_stride("v", v, q)
-    B, L, Hq, D = q.shape
-    Hkv = k.shape[2]
-    if k.shape != (B, L, Hkv, D) or v.shape != k.shape:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
-    if isinstance(positions, torch.Tensor) and positions.dim() == 2:
-        positions = positions.unsqueeze(0)
-    _need("positions", positions, torch.int32, 3, q)
-    _need("inv_freq", inv_freq, torch.float32, 1, q)
-    _need("slots", slots, torch.int32, 2, q)
-    n_axes, rot = positions.shape[0], 2 * inv_freq.shape[0]
-    if positions.shape != (n_axes, B, L) or slots.shape != (B, L):
-        raise ValueError("positions must be [n_axes,B,L] and slots [B,L]")
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.int8):
-        raise TypeError("k_cache must be a bfloat16, float8_e4m3fn or int8 tensor")
-    _need("k_cache", k_cache, k_cache.dtype, 4, q)
-    _need("v_cache", v_cache, k_cache.dtype, 4, q)
-    n_outer, Hkv2, rows, D2 = k_cache.shape
-    if Hkv2 != Hkv or D2 != D or v_cache.shape != k_cache.shape:
-        raise ValueError(f"the caches must be [n,{Hkv},rows,{D}]")
-    fmt, want = 0, None
-    if k_cache.dtype is torch.float8_e4m3fn:
-        fmt, sdt, want = _native.ATTN_KV_E4M3, torch.float32, (Hkv,)
-    elif k_cache.dtype is torch.int8:
-        fmt, sdt, want = _native.ATTN_KV_Q8_0, torch.float16, (n_outer, Hkv, rows, D // 32)
-    if (k_scale is None) != (fmt == 0) or (v_scale is None) != (fmt == 0):
-        raise ValueError("k_scale and v_scale go with an 8-bit cache, and only with one")
-    if fmt:
-        _need("k_scale", k_scale, sdt, len(want), q)
-        _need("v_scale", v_scale, sdt, len(want), q)
-        if k_scale.shape != want or v_scale.shape != want:
-            raise ValueError(f"k_scale and v_scale must have shape {want}")
-    sections = (rot // 2,) if sections is None else [_c_int("sections", x) for x in sections]
-    if len(sections) != n_axes:
-        raise ValueError(f"{n_axes} position axes need as many sections, got {len(sections)}")
     if axis_order not in ("blocks", "cycle") or pairs not in ("half", "adjacent"):
         raise ValueError("axis_order must be 'blocks' or 'cycle', pairs 'half' or 'adjacent'")
-    index = q.get_device()
-    with _on(index, stream):
-        out = _made("out", out, torch.bfloat16, (B, Hq, L, D), q)
-        st = _native.lib().attn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_step, k_step, v_step, positions.data_ptr(),
-                                            inv_freq.data_ptr(), slots.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
-                                            v_cache.data_ptr(), _at(k_scale), _at(v_scale), fmt, B, L, Hq, Hkv, D, rot, n_outer,
-                                            rows, n_axes, (ctypes.c_int * n_axes)(*sections), axis_order == "cycle",
-                                            pairs == "adjacent", torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        _native.check(st, "attn_rope_append")
-    return out
+    with _on(stream, q):
+        return _native.calls().rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, sections, axis_order == "cycle",
+                                           pairs == "adjacent", k_scale, v_scale, out)
 
 
 def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Tensor, accept: torch.Tensor,
@@ -847,33 +667,8 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Ten
     [n_pages,Hkv,page_size,D] with block_table int32 [B,max_pages]; seqlens int32 [B] with the tree's rows;
     accept int32 [B,A] the path's nodes, increasing, the first n_accept[b] of them taken.  T, tree_lens as in
     decode_tree.  Returns out_seqlens int32 [B] (may be seqlens): the rows before the tree plus n_accept."""
-    _check_tensor("k_cache", k_cache, torch.bfloat16, 4)
-    _need("v_cache", v_cache, torch.bfloat16, 4, k_cache)
-    _need("seqlens", seqlens, torch.int32, 1, k_cache)
-    _need("accept", accept, torch.int32, 2, k_cache)
-    _need("n_accept", n_accept, torch.int32, 1, k_cache)
-    B, T = seqlens.shape[0], _c_int("T", T)
-    if v_cache.shape != k_cache.shape or accept.shape[0] != B or n_accept.shape[0] != B:
-        raise ValueError("shape mismatch between the caches, seqlens, accept and n_accept")
-    max_pages, held = 0, k_cache.shape[0]
-    if block_table is not None:
-        _need("block_table", block_table, torch.int32, 2, k_cache)
-        held, max_pages = block_table.shape
-    if tree_lens is not None:
-        _need("tree_lens", tree_lens, torch.int32, 1, k_cache)
-    if held != B or (tree_lens is not None and tree_lens.shape[0] != B):
-        raise ValueError("shape mismatch between seqlens, the caches, block_table and tree_lens")
-    n_outer, Hkv, rows, D = k_cache.shape
-    index = k_cache.get_device()
-    with _on(index, stream):
-        out_seqlens = torch.empty_like(seqlens) if out_seqlens is None else _made("out_seqlens", out_seqlens, torch.int32, (B,), k_cache)
-        st = _native.lib().attn_tree_commit(k_cache.data_ptr(), v_cache.data_ptr(), _at(block_table), seqlens.data_ptr(),
-                                            _at(tree_lens), accept.data_ptr(), n_accept.data_ptr(), out_seqlens.data_ptr(), B, Hkv,
-                                            T, accept.shape[1], D, n_outer, rows, max_pages,
-                                            torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        _native.check(st, "attn_tree_commit")
-    return out_seqlens
+    with _on(stream, k_cache):
+        return _native.calls().tree_commit(k_cache, v_cache, seqlens, accept, n_accept, T, block_table, tree_lens, out_seqlens)
 
 
 def device_error(reset: bool = True) -> int:

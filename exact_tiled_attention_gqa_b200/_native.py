@@ -1,17 +1,19 @@
 """ctypes binding of include/attn_gqa.h -- argument marshalling only.
 
 Every call converts tensors to device pointers and sizes, passes the caller's
-CUDA stream, and raises ``AttnError`` on a non-zero status.  All computation
+CUDA stream, and raises ``AttnError`` on a non-zero status; the calls of a
+serving step go through the C++ module of ``csrc/torch_calls.cpp``.  All computation
 happens in the CUDA kernels of ``libattn_gqa_sm100.so``; there is no other
 path: if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
-from .build import DEBUG_LIB_PATH, LIB_PATH
+from .build import CALLS_PATH, DEBUG_LIB_PATH, LIB_PATH
 
 # ATTN_GQA_DEBUG_BOUNDS=1 in the environment loads the bounds-checking build of
 # the same sources instead (build.py, debug_bounds=True); tests use it.
@@ -111,6 +113,30 @@ def lib() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib = handle
     return _lib
+
+
+# the C functions csrc/torch_calls.cpp calls
+BOUND = ("attn_page_plan", "attn_page_release", "attn_rope_append", "attn_decode_tree", "attn_decode_tree_workspace_size",
+         "attn_decode_tree_paged", "attn_decode_tree_paged_workspace_size", "attn_tree_commit")
+
+_calls = None
+
+
+def calls():
+    """Load the C++ binding of the serving-step calls (built in-tree) and hand it the library's functions."""
+    global _calls
+    if _calls is None:
+        handle = lib()
+        with _lock:
+            if _calls is None:
+                if not os.path.exists(CALLS_PATH):
+                    raise RuntimeError(f"{CALLS_PATH} is missing: build it with `python -m exact_tiled_attention_gqa_b200.build`")
+                spec = importlib.util.spec_from_file_location(__package__ + "._torch_calls", CALLS_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.bind({name: ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in BOUND}, check)
+                _calls = module
+    return _calls
 
 
 def check(status: int, what: str) -> None:

@@ -4,6 +4,9 @@ One translation unit (csrc/attn_gqa.cu) compiled by nvcc for sm_100a only into
 ``libattn_gqa_sm100.so`` next to this file.  The runtime is linked statically,
 and cuTensorMapEncodeTiled is fetched through the runtime's driver entry point,
 so the library needs nothing beyond the CUDA driver at load time.
+
+Beside it the Python binding of the serving-step calls (csrc/torch_calls.cpp, a
+C++ module on torch's headers, no device code).
 """
 from __future__ import annotations
 
@@ -13,6 +16,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -23,6 +27,9 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 # unit mapping, ring positions, TMA coordinates and output indices and report a
 # violation as ATTN_DEVERR_BOUNDS (a checking build for tests, not for speed).
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libattn_gqa_sm100_debug_bounds.so")
+# the C++ binding of the serving-step calls, an importable module
+CALLS_PATH = os.path.join(PKG_DIR, "_torch_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -99,5 +106,39 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return path
 
 
+def _host_cxx() -> str:
+    """A g++ with the shared libstdc++, which torch uses too: one that links it in statically gives the module
+    stream classes of its own, and an error message with a number in it then crashes."""
+    for cand in (shutil.which("g++"), "/usr/bin/g++", os.environ.get("CXX")):
+        if cand and os.path.exists(cand):
+            found = subprocess.run([cand, "-print-file-name=libstdc++.so"], capture_output=True, text=True)
+            if os.path.isabs(found.stdout.strip()):
+                return cand
+    raise RuntimeError("no g++ with a shared libstdc++ found")
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile csrc/torch_calls.cpp against the running torch and Python."""
+    header = os.path.join(ROOT, "include", "attn_gqa.h")
+    if not force and os.path.exists(CALLS_PATH) and \
+            all(os.path.getmtime(s) <= os.path.getmtime(CALLS_PATH) for s in (CALLS_SOURCE, header)):
+        return CALLS_PATH
+    import torch
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    torch_dir = os.path.dirname(torch.__file__)
+    include, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = [_host_cxx(), "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{include}", f"-I{os.path.join(include, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda}", f"-I{sysconfig.get_paths()['include']}", CALLS_SOURCE, "-o", tmp,
+           f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, debug_bounds="--debug-bounds" in sys.argv))
+    print(build_calls(force="--force" in sys.argv))

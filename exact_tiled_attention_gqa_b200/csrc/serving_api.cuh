@@ -57,9 +57,10 @@ int launch_tree(const void* q, const void* kc, const void* vc, const TreeParams&
     if ((st = check_launch("attn_tree_kernel")) != ATTN_OK) return st;
     const long long pairs = static_cast<long long>(prm.B) * prm.Hkv, rows_per_pair = static_cast<long long>(prm.G) * prm.Lq;
     const long long slices = (rows_per_pair + kTreeCombineRows - 1) / kTreeCombineRows;
-    // a pair over more than 4 ranges: a CTA for each row
+    // a CTA for each row where that is at most four waves of one an SM (a few rows: 12.6 us a call by
+    // slices of 32, 10.4 by rows), or where a pair lies in more than 4 ranges
     const cudaError_t e =
-        lay.n_ranges > 4 * pairs
+        pairs * rows_per_pair <= 4 * 148 || lay.n_ranges > 4 * pairs
             ? launch_dependent(attn_tree_combine_many_kernel<D>, static_cast<unsigned>(pairs * rows_per_pair), 128u, stream, tp)
             : launch_dependent(attn_tree_combine_kernel<D>, static_cast<unsigned>(pairs * slices), 128u, stream, tp);
     if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "attn_tree_combine_kernel launch failed: %s", cudaGetErrorString(e));

@@ -7,7 +7,7 @@ import torch
 
 import exact_tiled_attention_gqa_b200 as attn
 from exact_tiled_attention_gqa_b200 import _native
-from exact_tiled_attention_gqa_b200.build import build
+from exact_tiled_attention_gqa_b200.build import build, build_calls
 
 # an aligned fake address, only ever passed together with an invalid argument
 A = ctypes.c_void_p(0x10000)
@@ -19,6 +19,7 @@ NULL = None
 @pytest.fixture(scope="module")
 def lib():
     build()
+    build_calls()
     return _native.lib()
 
 
@@ -163,7 +164,7 @@ def test_pack_tree_mask_rejects(bad):
         attn.pack_tree_mask(bad)
 
 
-def test_host_tensors_are_refused():
+def test_host_tensors_are_refused(lib):
     z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
@@ -177,3 +178,33 @@ def test_host_tensors_are_refused():
         attn.decode_tree(bf(1, 4, 3, 64), bf(1, 2, 64, 64), bf(1, 2, 64, 64), z(1), z(1, 3, 1))
     with pytest.raises(ValueError, match="CUDA"):
         attn.tree_commit(bf(1, 2, 64, 64), bf(1, 2, 64, 64), z(1), z(1, 2), z(1), T=3)
+
+
+def test_missing_binding_raises(monkeypatch, tmp_path):
+    monkeypatch.setattr(_native, "_calls", None)
+    monkeypatch.setattr(_native, "CALLS_PATH", str(tmp_path / "absent.so"))
+    with pytest.raises(RuntimeError, match="missing"):
+        _native.calls()
+
+
+def test_binding_reaches_the_loaded_library(lib):
+    """The C++ binding is handed the functions of the library ctypes loaded, and raises AttnError with its words."""
+    calls = _native.calls()
+    assert _native.calls() is calls and all(hasattr(lib, name) for name in _native.BOUND)
+    cpu = torch.zeros(1, dtype=torch.int32)
+    for bad in (None, 3, "x"):
+        with pytest.raises(TypeError):
+            calls.page_release(cpu, bad, cpu, cpu, cpu, 64, 8, None)
+
+
+def test_sizes_are_refused_with_words(lib):
+    """(Numbers in the binding's messages: a module with a C++ library of its own would crash on them.)"""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16)
+    for kw, words in ((dict(L=-1), "L=-1"), (dict(page_size=1 << 31), "page_size=2147483648"), (dict(n_pages=-7), "n_pages=-7")):
+        with pytest.raises(ValueError, match=words):
+            attn.page_plan(z(2), z(2), z(2, 4), z(8), z(1), **{**dict(L=1, page_size=64, n_pages=8), **kw})
+    with pytest.raises(ValueError, match="page_size=-64"):
+        attn.page_release(z(2), z(2), z(2, 4), z(8), z(1), page_size=-64, n_pages=8)
+    with pytest.raises(ValueError, match="T=-2"):
+        attn.tree_commit(bf, bf, z(1), z(1, 2), z(1), T=-2)
