@@ -355,12 +355,15 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
         }
         RingPos at;
         bool ok = true;
+        auto wait_bar = [&](uint32_t bar, uint32_t parity) {       // the warp goes on, or stops, together
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_attn_err, kDevErrTimeout)) != 0;
+        };
         TreeSeg s = first;
         do {
             const int n_tiles = s.t1 - s.t0;
             if (!L::kQTmem) {
                 // (the last Q K^T of a segment is issued two tiles before its end)
-                ok = mbar_wait(bar_q_empty, (s.n & 1) ^ 1u, abort_flag, &g_attn_err, kDevErrTimeout);
+                ok = wait_bar(bar_q_empty, (s.n & 1) ^ 1u);
                 if (!ok) break;
                 if (lane == 0) {
                     const size_t row0 = (static_cast<size_t>(s.b) * p.Hq + static_cast<size_t>(s.g) * p.G) * p.Lq + mblk * 128;
@@ -371,7 +374,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                 __syncwarp();
             }
             // Pages of the segment's 64-row boxes, a window of 32 in the warp's lanes and the next one
-            // on its way: looked up box by box, they held the loads back (64 requests: 977 us for 688).
+            // on its way: looked up box by box they held the loads back (with two boxes a tile, 978 us for 869
+            // at 64 requests of 1K to 32K rows).
             const int boxes_before = s.t0 * (kTile / 64), boxes_end = min(s.t1 * (kTile / 64), (s.seqlen + 63) / 64);
             int window = boxes_before, here = 0, after = 0;
             auto lookup = [&](int box0) {
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                     here = after;
                     after = lookup(window + 32);
                 }
-                ok = mbar_wait(bar_empty(at.e), at.par ^ 1u, abort_flag, &g_attn_err, kDevErrTimeout);
+                ok = wait_bar(bar_empty(at.e), at.par ^ 1u);
                 if (!ok) break;
                 if (lane == 0) {
                     if (ATTN_DEBUG_BOUNDS) ring_tag[at.e] = at.item;

@@ -580,6 +580,31 @@ def test_commit_refusals():
         attn.tree_commit(c, c.clone(), sl, acc, n, T=0)
 
 
+def test_empty_batches():
+    """No requests, no tokens: every call returns its empty results and touches nothing."""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    out, lse = attn.decode_tree(bf(0, 4, 3, 64), bf(0, 2, 9, 64), bf(0, 2, 9, 64), z(0), z(0, 3, 1))
+    assert out.shape == (0, 4, 3, 64) and lse.shape == (0, 4, 3)
+    out, lse = attn.decode_tree_paged(bf(0, 4, 3, 64), bf(2, 2, 64, 64), bf(2, 2, 64, 64), z(0, 3), z(0), z(3, 1))
+    assert out.shape == (0, 4, 3, 64)
+    pool = torch.ones(2, 2, 64, 64, dtype=torch.bfloat16, device="cuda")
+    for B, L in ((0, 5), (5, 0)):
+        q = attn.rope_append(bf(B, L, 4, 64), bf(B, L, 2, 64), bf(B, L, 2, 64), z(B, L), torch.ones(32, device="cuda"), z(B, L), pool, pool.clone())
+        assert q.shape == (B, 4, L, 64)
+    assert attn.tree_commit(pool, pool.clone(), z(0), z(0, 2), z(0), T=4, block_table=z(0, 2)).shape == (0,)
+    assert (pool == 1).all() and attn.device_error(reset=True) == 0
+
+
+def test_every_sequence_empty():
+    """Lengths of zero everywhere: nothing is read, every row is 0 and -inf."""
+    B, Hq, Hkv, T, D = 5, 12, 2, 30, 128
+    q = torch.full((B, Hq, T, D), NAN, dtype=torch.bfloat16, device="cuda")
+    c = torch.full((B, Hkv, 70, D), NAN, dtype=torch.bfloat16, device="cuda")
+    out, lse = attn.decode_tree(q, c, c, i32([0] * B), torch.full((T, 1), -1, dtype=torch.int32, device="cuda"))
+    assert attn.device_error(reset=True) == 0 and (out == 0).all() and (lse == -math.inf).all()
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
