@@ -191,14 +191,21 @@ int check_plan(const PlanParams& p) {
         return fail(ATTN_ERR_UNSUPPORTED, "block table or page stack too large");
     return ATTN_OK;
 }
-// Slots up to this many are written by attn_page_plan_kernel itself.
-constexpr long long kPlanSlots = 32768;
-// Table entries up to this many (at most, by the sizes) are copied by one CTA, more by a cluster.
-constexpr long long kPlanEntries = 4096;
+// attn_page_plan_kernel writes up to this many slots itself, a second kernel on the whole GPU more.  Device time
+// of the call, both ways, on the cluster: 8192 slots of 512 requests 5.1 and 6.0 us, 8192 of 64 5.3 and 5.5,
+// 16384 of 64 5.8 and 5.6, 32768 of 512 7.2 and 6.0.
+constexpr long long kPlanSlots = 8192;
+// One CTA does a step of up to so many requests and slots (64 requests of a row 4.1 us, on the cluster 4.5; of 16
+// rows 4.5 and 4.9), the cluster of eight larger ones (512 of a row 5.0 us, on one CTA 5.3; 64 of 64 rows 5.0 and 6.7).
+constexpr int kPlanOneB = 128;
+constexpr long long kPlanOneSlots = 1024;
+// page_release does not know how many pages go: one CTA where the tables are small, the cluster where they could be
+// many (512 requests of up to 256 pages 15.6 us on one CTA and 8.0; 64 requests of a few pages 4.0 and 4.4).
+constexpr long long kReleaseEntries = 4096;
 
-int launch_plan(void (*kernel)(const PlanParams), long long entries, cudaStream_t s, const PlanParams& p, const char* what) {
+int launch_plan(void (*kernel)(const PlanParams), bool one, cudaStream_t s, const PlanParams& p, const char* what) {
     cudaLaunchAttribute attr[1];
-    const unsigned n = entries > kPlanEntries ? kPlanCluster : 1;
+    const unsigned n = one ? 1 : kPlanCluster;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = n;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -229,9 +236,9 @@ extern "C" int attn_page_plan(const int32_t* seqlens, const int32_t* new_lens, i
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long n = static_cast<long long>(B) * L;
     const bool slots_too = n <= kPlanSlots;
-    const long long entries = static_cast<long long>(B) * std::min(max_pages, L / page_size + 1);
-    if ((st = slots_too ? launch_plan(attn_page_plan_kernel<true>, entries, s, p, "attn_page_plan_kernel")
-                        : launch_plan(attn_page_plan_kernel<false>, entries, s, p, "attn_page_plan_kernel")) != ATTN_OK)
+    const bool one = B <= kPlanOneB && n <= kPlanOneSlots;
+    if ((st = slots_too ? launch_plan(attn_page_plan_kernel<true>, one, s, p, "attn_page_plan_kernel")
+                        : launch_plan(attn_page_plan_kernel<false>, one, s, p, "attn_page_plan_kernel")) != ATTN_OK)
         return st;
     if (!slots_too) {
         const long long units = static_cast<long long>(B) * ((L + static_cast<long long>(kSlotRun) - 1) / kSlotRun);
@@ -250,7 +257,7 @@ extern "C" int attn_page_release(const int32_t* seqlens, const int32_t* keep_len
                     out_n_free, nullptr, B, 0, page_size, max_pages, capacity, n_pages};
     int st = check_plan(p);
     if (st != ATTN_OK) return st;
-    st = launch_plan(attn_page_release_kernel, static_cast<long long>(B) * max_pages, static_cast<cudaStream_t>(stream), p,
+    st = launch_plan(attn_page_release_kernel, static_cast<long long>(B) * max_pages <= kReleaseEntries, static_cast<cudaStream_t>(stream), p,
                      "attn_page_release_kernel");
     return st == ATTN_OK ? ok() : st;
 }

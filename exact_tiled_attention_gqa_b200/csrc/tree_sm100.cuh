@@ -27,6 +27,17 @@
 // takes half the TMEM, one CTA on an SM; Q lies in TMEM, which leaves its 64 KB of shared
 // memory to K and V.
 //
+// What bounds it, one B200.  64 requests of 1K to 32K rows, 32 heads over 8 KV heads, 16 nodes, head
+// dim 128 (4.45 GB, 687 us at the copy rate): the CTAs take 625 to 655 us, 6.9 TB/s, the cache read;
+// the same at 1.5 and 1.6 GHz.  A grid of splits of the longest cache instead of equal ranges took
+// 838 us.  8 requests of 3K to 16K rows, 32 heads over 4, 63 nodes, head dim 256 (four query blocks;
+// 117 GFLOP, 70 us at the bf16 rate): 160 us for a CTA of one segment and 12 more for each further
+// one, about 2260 cycles a tile.  The MMAs are 1376 of them (an MMA of N = 64 costs 54 cycles, not
+// 32); what is left is the issuing warp going from one commit to the next wait.  Not faster: tiles
+// of 128 rows in two streams, each with a softmax warpgroup, on one CTA an SM (head dim 128, 770 us
+// for 683); looking for P and V half-way through Q K^T; waiting for K and V under P V (342K cycles
+// for 306K); head dim 256 with Q in shared memory (331K for 306K, with a shallower ring).
+//
 // The mask costs nothing over the committed rows: only a tile that reaches past c builds the
 // 64 visibility bits of its rows, each thread (one query row) shifting them out of its own
 // mask words.
