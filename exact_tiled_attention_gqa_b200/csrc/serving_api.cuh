@@ -29,7 +29,7 @@ TreeLayout tree_layout(int B, int Hq, int Hkv, int T, int Lmax, int D) {
     t.n_mblk = static_cast<int>((rg + 127) / 128);
     const long long tiles = static_cast<long long>(B) * Hkv * ((Lmax + 63LL) / 64);
     const long long ctas = 148LL * (D == 256 ? TreeCfg<256>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
-    t.n_ranges = static_cast<int>(std::max(1LL, std::min(ctas / t.n_mblk, (tiles + 1) / 2)));
+    t.n_ranges = static_cast<int>(std::max(1LL, std::min(ctas / t.n_mblk, tiles)));
     const size_t rows = static_cast<size_t>(t.n_ranges) * t.n_mblk * 2 * static_cast<size_t>(std::min(128LL, rg));
     t.lse_off = align256(rows * D * sizeof(float));
     t.tiles_off = t.lse_off + align256(rows * sizeof(float));
@@ -57,12 +57,17 @@ int launch_tree(const void* q, const void* kc, const void* vc, const TreeParams&
     if ((st = check_launch("attn_tree_kernel")) != ATTN_OK) return st;
     const long long pairs = static_cast<long long>(prm.B) * prm.Hkv, rows_per_pair = static_cast<long long>(prm.G) * prm.Lq;
     const long long slices = (rows_per_pair + kTreeCombineRows - 1) / kTreeCombineRows;
-    // a CTA for each row where that is at most four waves of one an SM (a few rows: 12.6 us a call by
-    // slices of 32, 10.4 by rows), or where a pair lies in more than 4 ranges
+    // n_ranges / pairs, at most the partials of a pair on average, decides how the combine spreads them.  Over the warps
+    // against all by one: 8 requests of 9000 rows, 63 nodes, D 64 (32 pairs) 66 us and 61; 6 of 6000 rows, 21 nodes, 8 heads
+    // a KV head, D 128 (12 pairs) 7.7 us of combine, by four columns a lane 13.4; 4 rows on 12000 12.8 us a call by four
+    // columns a lane, by rows 15.3.
+    const unsigned few_rows = static_cast<unsigned>(pairs * ((rows_per_pair * (D / 4) + 31) / 32));
+    const unsigned one = static_cast<unsigned>(pairs * slices * (D / 64)), four = static_cast<unsigned>(pairs * slices * (D / 16));
     const cudaError_t e =
-        pairs * rows_per_pair <= 4 * 148 || lay.n_ranges > 4 * pairs
-            ? launch_dependent(attn_tree_combine_many_kernel<D>, static_cast<unsigned>(pairs * rows_per_pair), 128u, stream, tp)
-            : launch_dependent(attn_tree_combine_kernel<D>, static_cast<unsigned>(pairs * slices), 128u, stream, tp);
+        rows_per_pair < kTreeCombineRows && lay.n_ranges > pairs
+            ? launch_dependent(attn_tree_combine_few_rows_kernel<D>, few_rows, 128u, stream, tp)
+        : lay.n_ranges > 4 * pairs ? launch_dependent(attn_tree_combine_kernel<D, 4>, four, 128u, stream, tp)
+                                   : launch_dependent(attn_tree_combine_kernel<D, 1>, one, 128u, stream, tp);
     if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "attn_tree_combine_kernel launch failed: %s", cudaGetErrorString(e));
     return check_launch("attn_tree_combine_kernel");
 }

@@ -28,10 +28,10 @@
 // memory to K and V.
 //
 // What bounds it, one B200.  64 requests of 1K to 32K rows, 32 heads over 8 KV heads, 16 nodes, head
-// dim 128 (4.45 GB, 687 us at the copy rate): the CTAs take 625 to 655 us, 6.9 TB/s, the cache read;
+// dim 128 (4.45 GB, 687 us at the copy rate): the CTAs take 625 to 655 us, 6.9 TB/s, the cache read,
 // the same at 1.5 and 1.6 GHz.  A grid of splits of the longest cache instead of equal ranges took
 // 838 us.  8 requests of 3K to 16K rows, 32 heads over 4, 63 nodes, head dim 256 (four query blocks;
-// 117 GFLOP, 70 us at the bf16 rate): 160 us for a CTA of one segment and 12 more for each further
+// 117 GFLOP, 70 us at the bf16 rate): 156 us for a CTA of one segment and 10 more for each further
 // one, about 2260 cycles a tile.  The MMAs are 1376 of them (an MMA of N = 64 costs 54 cycles, not
 // 32); what is left is the issuing warp going from one commit to the next wait.  Not faster: tiles
 // of 128 rows in two streams, each with a softmax warpgroup, on one CTA an SM (head dim 128, 770 us
@@ -79,10 +79,18 @@ __device__ __forceinline__ int tree_tiles(int seqlen) {
     return seqlen / TILE + (seqlen % TILE != 0);
 }
 
-// Row r of the partial that range `range` wrote for query block mblk in slot 0 (its first
-// segment) or 1 (its last).
-__device__ __forceinline__ size_t tree_part(const TreeParams& p, long long range, int mblk, int slot, int r) {
-    return ((static_cast<size_t>(range) * p.n_mblk + mblk) * 2 + slot) * min(128, p.d.G * p.d.Lq) + r;
+// The partial that range `range` wrote for query block mblk in slot 0 (its first segment) or 1
+// (its last), of min(128, G x T) rows.
+__device__ __forceinline__ size_t tree_part(const TreeParams& p, long long range, int mblk, int slot) {
+    return (static_cast<size_t>(range) * p.n_mblk + mblk) * 2 + slot;
+}
+
+// Element (row r, column c) of a partial of `box` rows: four columns of all rows, then the next four,
+// so that the epilogue (a thread per row) writes, and the combine (a lane per row) reads, 512
+// contiguous bytes a warp.  (Row after row, a warp's stores met 32 lines each: two requests of 1500
+// and 3000 rows, 16 nodes, head dim 256 took 30 us for 24.)
+__device__ __forceinline__ size_t tree_part_at(int box, int r, int c) {
+    return (static_cast<size_t>(c >> 2) * box + r) * 4 + (c & 3);
 }
 
 __device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
@@ -131,17 +139,18 @@ __device__ __forceinline__ size_t tree_cache_row(const DecodeParams& p, int b, i
 
 // Adds the non-finite elements of the tree rows in [k_begin, k_end) that this
 // thread's node sees to its output or partial (any positive weight times them is
-// themselves).
+// themselves); element c of the row at dst[(c / 4) step + c % 4].
 template <typename T>
 __device__ __noinline__ void tree_add_nonfinite(const TreeParams& tp, int b, int g, const uint32_t* words, int ctx,
-                                                int k_begin, int k_end, int D, T* dst) {
+                                                int k_begin, int k_end, int D, T* dst, int step) {
     for (int row = max(max(ctx, 0), k_begin); row < k_end; ++row) {
         const int j = row - ctx;
         if (!(words[j >> 5] >> (j & 31) & 1u)) continue;
         const __nv_bfloat16* src = tp.v + tree_cache_row(tp.d, b, g, row) * D;
         for (int c = 0; c < D; ++c) {
             const float x = __bfloat162float(src[c]);
-            if (!isfinite(x)) dst[c] = static_cast<T>(static_cast<float>(dst[c]) + x);
+            T& y = dst[static_cast<size_t>(c >> 2) * step + (c & 3)];
+            if (!isfinite(x)) y = static_cast<T>(static_cast<float>(y) + x);
         }
     }
 }
@@ -212,6 +221,24 @@ __device__ __forceinline__ bool tree_next(const TreeParams& tp, TreeSeg& s) {
     return true;
 }
 
+// Tiles that a range has at least, where there are fewer than the GPU could hold ranges for.  Longer
+// ranges cost a tile's time each, shorter ones partials: their bytes, written and read, and rounds of
+// 32 of a pair's partials in the combine.  With r tiles a range the sum is t r + c / r, least at
+// r = sqrt(c / t); t, the byte rate and a round's time are fitted to the device times of ten small
+// trees with r = 1, 2 and 4, of which it takes the fastest or one within 0.1 us: one request of 375
+// rows, 8 nodes of 32 heads, D 64 9.8 us (r = 1) for 10.5 (2) and 12.8 (4); 64 nodes of 8 heads of one
+// KV head on 6000 rows 15.6 (4) for 20.7 (1, 2); 4 rows on 12000 12.8 (2) for 16.3 (1) and 13.7 (4);
+// D 256, two requests of 1500 and 3000 rows 19.2 (1) for 24.2 (2).
+template <int D>
+__device__ __forceinline__ long long tree_least_tiles(const TreeParams& tp, long long total) {
+    constexpr float kTileUs = D == 256 ? 4.0f : 0.75f, kBytesPerUs = 5e6f, kRoundUs = 0.7f;
+    const float tiles = static_cast<float>(total);
+    const float bytes = tiles * static_cast<float>(tp.d.G * tp.d.Lq) * static_cast<float>(D * 4 * 2);
+    const float rounds = tiles / (static_cast<float>(tp.d.B) * static_cast<float>(tp.d.Hkv)) / 32.0f;
+    const float r = sqrtf((bytes / kBytesPerUs + rounds * kRoundUs) / kTileUs);
+    return max(1ll, static_cast<long long>(r + 0.5f));
+}
+
 template <int D>
 __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -251,7 +278,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
         total += s_warp[w];
     }
     total *= p.Hkv;
-    const long long per = max((total + tp.n_ranges - 1) / tp.n_ranges, 2ll);   // (a tile's softmax costs less than a partial)
+    const long long per = max((total + tp.n_ranges - 1) / tp.n_ranges, tree_least_tiles<D>(tp, total));
     if (blockIdx.x == 0) {                        // for the combine
         long long t = before;
         for (int b = my_b; b < my_end; ++b) {
@@ -583,14 +610,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
             if constexpr (L::kQTmem) {
                 // Q's row to TMEM (the last S of the segment before is complete, so its Q is used)
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
+                uint4 x[D / 8];
 #pragma unroll
-                for (int c = 0; c < D / 64; c += 2) {
-                    uint4 x[16];
+                for (int i = 0; i < D / 8; ++i) x[i] = r < R ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = r < R ? __ldg(src + c * 8 + i) : make_uint4(0, 0, 0, 0);
-                    tmem_st_32x32b_x32(tmem + L::kTmemQ + lane_off + c * 32, reinterpret_cast<const uint32_t*>(x));
-                    tmem_st_32x32b_x32(tmem + L::kTmemQ + lane_off + c * 32 + 32, reinterpret_cast<const uint32_t*>(x) + 32);
-                }
+                for (int i = 0; i < D / 8; i += 8)
+                    tmem_st_32x32b_x32(tmem + L::kTmemQ + lane_off + i * 4, reinterpret_cast<const uint32_t*>(x + i));
                 tmem_wait_st();
                 tc_fence_before_sync();
                 mbar_arrive(bar_q_full);
@@ -721,9 +746,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                 const bool seen = live && !(l_exact == 0.0f);
                 const float inv_l = seen ? 1.0f / l_run : 0.0f;
                 const float lse2 = seen ? m_run + __log2f(l_exact) : -INFINITY;
-                const size_t prow = tree_part(tp, range, mblk, s.n == 0 ? 0 : 1, row_valid ? r : 0);
+                const size_t part = tree_part(tp, range, mblk, s.n == 0 ? 0 : 1);
+                float* const o_part = p.o_part + part * box * D + tree_part_at(box, row_valid ? r : 0, 0);
                 ATTN_CHECK(row < static_cast<size_t>(p.B) * p.Hq * p.Lq);
-                ATTN_CHECK(whole || prow < static_cast<size_t>(tp.n_ranges) * tp.n_mblk * 2 * box);
+                ATTN_CHECK(whole || part < static_cast<size_t>(tp.n_ranges) * tp.n_mblk * 2);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -741,22 +767,22 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                                 make_uint4(pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]),
                                            pack_bf16x2(x[k + 4], x[k + 5]), pack_bf16x2(x[k + 6], x[k + 7]));
                     } else if (row_valid) {
-                        float* dst = p.o_part + prow * D + c;
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                            *reinterpret_cast<float4*>(o_part + static_cast<size_t>(c + k) * box) =
+                                make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                     }
                 }
                 // elements that the node sees and that are not finite
                 if (seen && v_patched[s.n & 1] == s.n + 1) {
                     if (whole)
-                        tree_add_nonfinite(tp, s.b, s.g, words, ctx, 0, k_end, D, tp.out + row * D);
+                        tree_add_nonfinite(tp, s.b, s.g, words, ctx, 0, k_end, D, tp.out + row * D, 4);
                     else
-                        tree_add_nonfinite(tp, s.b, s.g, words, ctx, s.t0 * kTile, k_end, D, p.o_part + prow * D);
+                        tree_add_nonfinite(tp, s.b, s.g, words, ctx, s.t0 * kTile, k_end, D, o_part, box * 4);
                 }
                 if (row_valid) {
                     if (!whole)
-                        p.lse_part[prow] = lse2;
+                        p.lse_part[part * box + r] = lse2;
                     else if (tp.lse != nullptr)
                         tp.lse[row] = lse2 * kLn2;
                 }
@@ -778,162 +804,185 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
 
 // Where the partials of a (sequence, KV head) pair lie.
 struct TreeParts {
-    long long start, per, r0;      // the pair's first tile in the line; tiles a range; first range
-    int n;                         // partials; 0: the sequence has no rows, 1: the result is written
+    long long r0;             // their first range
+    int n;                    // how many; 0: the sequence has no rows, 1: the result is written
+    bool late;                // the first one is its range's last segment
+
+    template <int TILE>
+    __device__ __forceinline__ void find(const TreeParams& tp, int pair) {
+        const int b = pair / tp.d.Hkv, g = pair - b * tp.d.Hkv;
+        const int tiles = tree_tiles<TILE>(decode_seqlen(tp.d, b));
+        const long long per = tp.tiles_before[tp.d.B];
+        const long long start = tp.tiles_before[b] * tp.d.Hkv + static_cast<long long>(g) * tiles;
+        r0 = 0;
+        n = 0;
+        late = false;
+        if (tiles > 0) {
+            r0 = start / per;
+            n = static_cast<int>((start + tiles - 1) / per - r0) + 1;
+            late = start != r0 * per;
+        }
+    }
+    // partial k of query block mblk (past the last one: the last one)
+    __device__ __forceinline__ size_t at(const TreeParams& tp, int k, int mblk) const {
+        k = min(k, n - 1);
+        return tree_part(tp, r0 + k, mblk, k == 0 && late ? 1 : 0);
+    }
 };
 
-template <int TILE>
-__device__ __forceinline__ TreeParts tree_parts(const TreeParams& tp, int b, int g) {
-    TreeParts q;
-    const int tiles = tree_tiles<TILE>(decode_seqlen(tp.d, b));
-    q.per = tp.tiles_before[tp.d.B];
-    q.start = tp.tiles_before[b] * tp.d.Hkv + static_cast<long long>(g) * tiles;
-    q.r0 = 0;
-    q.n = 0;
-    if (tiles > 0) {
-        q.r0 = q.start / q.per;
-        q.n = static_cast<int>((q.start + tiles - 1) / q.per - q.r0) + 1;
-    }
-    return q;
-}
-
-__device__ __forceinline__ size_t tree_part_row(const TreeParams& tp, const TreeParts& q, int k, int mblk, int r) {
-    return tree_part(tp, q.r0 + k, mblk, k == 0 && q.start != q.r0 * q.per ? 1 : 0, r);
-}
-
-// Running maximum, sum and O of one row's partials; kPer columns a lane.
-template <int kPer>
+// Running maximum, sum and O (C groups of four columns) of one row's partials.
+template <int C>
 struct TreeMerge {
-    float M = -INFINITY, sum = 0.0f, acc[kPer] = {};
+    float M = -INFINITY, sum = 0.0f;
+    float4 acc[C] = {};
 
+    __device__ __forceinline__ void scale(float f) {
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
+    }
+    // weight w: a partial that saw nothing has 0 and may hold anything
+    __device__ __forceinline__ void add(float w, float part_sum, const float4 (&o)[C]) {
+        sum = w == 0.0f ? sum : fmaf(w, part_sum, sum);
+        if (w != 0.0f) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                acc[i] = make_float4(fmaf(w, o[i].x, acc[i].x), fmaf(w, o[i].y, acc[i].y), fmaf(w, o[i].z, acc[i].z),
+                                     fmaf(w, o[i].w, acc[i].w));
+        }
+    }
     template <int N>
-    __device__ __forceinline__ void add(const float (&ls)[N], const float (&ov)[N][kPer]) {
+    __device__ __forceinline__ void add(const float (&ls)[N], const float4 (&ov)[N][C]) {
         float top = M;
 #pragma unroll
         for (int u = 0; u < N; ++u) top = fmaxf(top, ls[u]);
-        const float f = M == -INFINITY ? 1.0f : ex2_approx(M - top);   // (M = -inf: sum is 0, or NaN to stay)
+        scale(M == -INFINITY ? 1.0f : ex2_approx(M - top));   // (M = -inf: sum is 0, or NaN to stay)
         M = top;
-        sum *= f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] *= f;
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const float w = ls[u] == -INFINITY ? 0.0f : ex2_approx(ls[u] - M);
-            sum += w;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] = w == 0.0f ? acc[i] : fmaf(w, ov[u][i], acc[i]);
-        }
+        for (int u = 0; u < N; ++u) add(ls[u] == -INFINITY ? 0.0f : ex2_approx(ls[u] - M), 1.0f, ov[u]);
     }
     // a sum of 0: the row saw nothing; NaN: a score was
-    __device__ __forceinline__ void store(const TreeParams& tp, size_t row, int D, int lane) const {
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        __nv_bfloat16* o = tp.out + row * D + lane * kPer;
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(o + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-        if (tp.lse != nullptr && lane == 0) tp.lse[row] = sum == 0.0f ? -INFINITY : (M + __log2f(sum)) * kLn2;
-    }
+    __device__ __forceinline__ float lse() const { return sum == 0.0f ? -INFINITY : (M + __log2f(sum)) * kLn2; }
+    __device__ __forceinline__ float inv() const { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 };
 
-template <int kPer>
-__device__ __forceinline__ void load_cols(const float* src, float (&x)[kPer]) {
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + i);
-        x[i] = v.x;
-        x[i + 1] = v.y;
-    }
-}
-
-// out = sum_k 2^(lse_k - lse) O_k, lse = log2 sum_k 2^lse_k over the partials of a (sequence,
-// KV head) pair that lies in several ranges; rows of sequences without rows get 0 and -inf;
-// the rows of other pairs are there already.  A CTA takes 32 rows of a pair's query block, a
-// warp eight of them, kRows at a time and two partials of each (a pair has few).
+// out = sum_k 2^(lse_k - lse) O_k, lse = log2 sum_k 2^lse_k over the partials of a pair that lies in
+// several ranges; rows of sequences without rows get 0 and -inf; the rows of other pairs are there
+// already.  A lane takes a row, a warp 16 columns of 32 rows.  WPP = 1: all partials, two at a time,
+// the CTA's four warps 64 columns.  WPP = 4: every fourth partial, four at a time, the CTA's warps the
+// same 16 columns; they meet in shared memory.
 constexpr int kTreeCombineRows = 32;
 
-template <int D>
+template <int D, int WPP>
 __global__ void __launch_bounds__(128) attn_tree_combine_kernel(const TreeParams tp) {
     grid_dep_wait();   // launched as a programmatic dependent of attn_tree_kernel
-    constexpr int kPer = D / 32, kRows = D == 256 ? 2 : 4;
+    constexpr int kColCtas = D / 16 / (4 / WPP), C = 4, kInFlight = WPP == 1 ? 2 : 4;
     const DecodeParams& p = tp.d;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int RG = p.G * p.Lq;
+    const int RG = p.G * p.Lq, box = min(128, RG);
     const int slices = (RG + kTreeCombineRows - 1) / kTreeCombineRows;      // (128 is a multiple of their rows)
-    const int pair = blockIdx.x / slices, rr0 = (blockIdx.x - pair * slices) * kTreeCombineRows + warp * 8;
-    const int b = pair / p.Hkv, g = pair - b * p.Hkv;
-    const TreeParts q = tree_parts<TreeCfg<D>::kTile>(tp, b, g);
-    if (q.n == 1) return;
-    const size_t row0 = static_cast<size_t>(pair) * RG;
-    for (int u0 = 0; u0 < 8; u0 += kRows) {
-        TreeMerge<kPer> m[kRows];
-        for (int k0 = 0; k0 < q.n; k0 += 2) {
-            float ls[kRows][2], ov[kRows][2][kPer];
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int rr = min(rr0 + u0 + u, RG - 1);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    // (past the last partial: it again, with weight 0)
-                    const size_t at = tree_part_row(tp, q, min(k0 + k, q.n - 1), rr / 128, rr % 128);
-                    ls[u][k] = k0 + k < q.n ? p.lse_part[at] : -INFINITY;
-                    load_cols<kPer>(p.o_part + at * D + lane * kPer, ov[u][k]);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) m[u].add(ls[u], ov[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u)
-            if (rr0 + u0 + u < RG) m[u].store(tp, row0 + rr0 + u0 + u, D, lane);
-    }
-}
-
-// The same for pairs over many ranges: a CTA takes one row, its four warps every fourth
-// partial, eight at a time; their sums meet in shared memory.
-template <int D>
-__global__ void __launch_bounds__(128) attn_tree_combine_many_kernel(const TreeParams tp) {
-    grid_dep_wait();
-    constexpr int kPer = D / 32, kInFlight = 8;
-    const DecodeParams& p = tp.d;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x, RG = p.G * p.Lq;
-    const int pair = row / RG, rr = row - pair * RG;
-    const int b = pair / p.Hkv, g = pair - b * p.Hkv;
-    const TreeParts q = tree_parts<TreeCfg<D>::kTile>(tp, b, g);
-    if (q.n == 1) return;                          // uniform over the CTA
-    TreeMerge<kPer> m;
-    for (int k0 = warp; k0 < q.n; k0 += 4 * kInFlight) {
-        float ls[kInFlight], ov[kInFlight][kPer];
+    const int unit = blockIdx.x / kColCtas, pair = unit / slices;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = WPP == 1 ? 0 : warp;
+    const int rr = (unit - pair * slices) * kTreeCombineRows + lane;
+    const int col0 = (static_cast<int>(blockIdx.x % kColCtas) * (4 / WPP) + (WPP == 1 ? warp : 0)) * 16;
+    TreeParts parts;
+    parts.find<TreeCfg<D>::kTile>(tp, pair);
+    if (parts.n == 1) return;                      // uniform over the CTA
+    const int row = min(rr, RG - 1), mblk = row / 128, r = row % 128;
+    TreeMerge<C> m;
+    for (int k0 = sub; k0 < parts.n; k0 += WPP * kInFlight) {
+        float ls[kInFlight];
+        float4 ov[kInFlight][C];
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int k = k0 + 4 * u;
-            const size_t at = tree_part_row(tp, q, min(k, q.n - 1), rr / 128, rr % 128);
-            ls[u] = k < q.n ? p.lse_part[at] : -INFINITY;
-            load_cols<kPer>(p.o_part + at * D + lane * kPer, ov[u]);
+            const int k = k0 + u * WPP;
+            const size_t part = parts.at(tp, k, mblk);
+            ls[u] = k < parts.n ? p.lse_part[part * box + r] : -INFINITY;
+            const float* src = p.o_part + part * box * D + tree_part_at(box, r, col0);
+#pragma unroll
+            for (int i = 0; i < C; ++i) ov[u][i] = *reinterpret_cast<const float4*>(src + static_cast<size_t>(i) * box * 4);
         }
         m.add(ls, ov);
     }
-    __shared__ float s_m[4], s_sum[4], s_acc[4][D];
+    if constexpr (WPP > 1) {
+        __shared__ float s_m[WPP][32], s_sum[WPP][32];
+        __shared__ float4 s_acc[WPP][C][32];
+        s_m[warp][lane] = m.M;
+        s_sum[warp][lane] = m.sum;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = m.acc[i];
-    if (lane == 0) {
-        s_m[warp] = m.M;
-        s_sum[warp] = m.sum;
+        for (int i = 0; i < C; ++i) s_acc[warp][i][lane] = m.acc[i];
+        __syncthreads();
+        if (warp != 0) return;
+        m = TreeMerge<C>();
+#pragma unroll
+        for (int w = 0; w < WPP; ++w) m.M = fmaxf(m.M, s_m[w][lane]);
+#pragma unroll
+        for (int w = 0; w < WPP; ++w) {
+            float4 o[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] = s_acc[w][i][lane];
+            m.add(s_m[w][lane] == -INFINITY ? 1.0f : ex2_approx(s_m[w][lane] - m.M), s_sum[w][lane], o);   // (-inf: sum 0, or NaN)
+        }
     }
-    __syncthreads();
-    if (warp != 0) return;
-    float top = m.M;
+    if (rr >= RG) return;
+    const float inv = m.inv();
+    const size_t orow = static_cast<size_t>(pair) * RG + rr;
+    uint4* o = reinterpret_cast<uint4*>(tp.out + orow * D + col0);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, s_m[w]);
-    TreeMerge<kPer> all;
-    all.M = top;
+    for (int i = 0; i < C; i += 2)
+        o[i / 2] = make_uint4(pack_bf16x2(m.acc[i].x * inv, m.acc[i].y * inv), pack_bf16x2(m.acc[i].z * inv, m.acc[i].w * inv),
+                              pack_bf16x2(m.acc[i + 1].x * inv, m.acc[i + 1].y * inv),
+                              pack_bf16x2(m.acc[i + 1].z * inv, m.acc[i + 1].w * inv));
+    if (tp.lse != nullptr && col0 == 0) tp.lse[orow] = m.lse();
+}
+
+// The same for pairs of fewer rows than a warp has lanes: a lane takes four columns of a row (32 lanes:
+// neighbours in the partial, whatever its rows), the CTA's four warps every fourth partial, eight at a
+// time, and they meet in shared memory.
+template <int D>
+__global__ void __launch_bounds__(128) attn_tree_combine_few_rows_kernel(const TreeParams tp) {
+    grid_dep_wait();
+    constexpr int kInFlight = 8;
+    const DecodeParams& p = tp.d;
+    const int RG = p.G * p.Lq, box = min(128, RG), groups = box * (D / 4), ctas = (groups + 31) / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.x / ctas, pair = unit / tp.n_mblk, mblk = unit - pair * tp.n_mblk;
+    const int e = min(static_cast<int>(blockIdx.x - unit * ctas) * 32 + lane, groups - 1), c4 = e / box, r = e - c4 * box;
+    TreeParts parts;
+    parts.find<TreeCfg<D>::kTile>(tp, pair);
+    if (parts.n == 1) return;                      // uniform over the CTA
+    TreeMerge<1> m;
+    for (int k0 = warp; k0 < parts.n; k0 += 4 * kInFlight) {
+        float ls[kInFlight];
+        float4 ov[kInFlight][1];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int k = k0 + 4 * u;
+            const size_t part = parts.at(tp, k, mblk);
+            ls[u] = k < parts.n ? p.lse_part[part * box + r] : -INFINITY;
+            ov[u][0] = *reinterpret_cast<const float4*>(p.o_part + (part * box * (D / 4) + e) * 4);
+        }
+        m.add(ls, ov);
+    }
+    __shared__ float s_m[4][32], s_sum[4][32];
+    __shared__ float4 s_acc[4][32];
+    s_m[warp][lane] = m.M;
+    s_sum[warp][lane] = m.sum;
+    s_acc[warp][lane] = m.acc[0];
+    __syncthreads();
+    if (warp != 0 || mblk * 128 + r >= RG) return;
+    TreeMerge<1> all;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) all.M = fmaxf(all.M, s_m[w][lane]);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        const float f = s_m[w] == -INFINITY ? 1.0f : ex2_approx(s_m[w] - top);   // (-inf: sum 0, or NaN)
-        all.sum += s_sum[w] * f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) all.acc[i] = f == 0.0f ? all.acc[i] : fmaf(f, s_acc[w][lane * kPer + i], all.acc[i]);
+        const float4 o[1] = {s_acc[w][lane]};
+        all.add(s_m[w][lane] == -INFINITY ? 1.0f : ex2_approx(s_m[w][lane] - all.M), s_sum[w][lane], o);   // (-inf: sum 0, or NaN)
     }
-    all.store(tp, row, D, lane);
+    const float inv = all.inv();
+    const size_t orow = static_cast<size_t>(pair) * RG + mblk * 128 + r;
+    *reinterpret_cast<uint2*>(tp.out + orow * D + c4 * 4) =
+        make_uint2(pack_bf16x2(all.acc[0].x * inv, all.acc[0].y * inv), pack_bf16x2(all.acc[0].z * inv, all.acc[0].w * inv));
+    if (tp.lse != nullptr && c4 == 0) tp.lse[orow] = all.lse();
 }
 
 }  // namespace attn
