@@ -53,7 +53,14 @@ void bind(const py::dict& addresses, const py::object& check) {
     check_status = check.inc_ref().ptr();
 }
 
-void done(int status, const char* what) {
+// The C call f(), without the interpreter's lock (a launch can wait for the device).
+template <typename F>
+void call(const char* what, F f) {
+    int status;
+    {
+        const py::gil_scoped_release unlocked;
+        status = f();
+    }
     if (status != ATTN_OK) py::reinterpret_borrow<py::object>(check_status)(status, what);
 }
 
@@ -123,10 +130,11 @@ std::tuple<Tensor, Tensor, Tensor, Tensor> page_plan(const Tensor& seqlens, cons
     const c10::cuda::CUDAGuard guard(dev);
     Tensor slots = result("slots", slots_, at::kInt, {B, L}, dev), lens = result("out_seqlens", out_seqlens_, at::kInt, {B}, dev);
     Tensor left = result("out_n_free", out_n_free_, at::kInt, {1}, dev), status = result("status", status_, at::kInt, {B}, dev);
-    done(calls.page_plan(ptr(seqlens), ptr(new_lens), ptr(table), ptr(free_pages), ptr(n_free), ptr(slots), ptr(lens), ptr(left),
-                         ptr(status), to_int("B", B), l, page, to_int("max_pages", table.size(1)),
-                         to_int("capacity", free_pages.size(0)), pages, current_stream(dev)),
-         "attn_page_plan");
+    call("attn_page_plan", [&] {
+        return calls.page_plan(ptr(seqlens), ptr(new_lens), ptr(table), ptr(free_pages), ptr(n_free), ptr(slots), ptr(lens), ptr(left),
+                               ptr(status), to_int("B", B), l, page, to_int("max_pages", table.size(1)),
+                               to_int("capacity", free_pages.size(0)), pages, current_stream(dev));
+    });
     return {slots, lens, left, status};
 }
 
@@ -137,10 +145,11 @@ Tensor page_release(const Tensor& seqlens, const Tensor& keep_lens, const Tensor
     const c10::Device dev = seqlens.device();
     const c10::cuda::CUDAGuard guard(dev);
     Tensor left = result("out_n_free", out_n_free_, at::kInt, {1}, dev);
-    done(calls.page_release(ptr(seqlens), ptr(keep_lens), ptr(table), ptr(free_pages), ptr(n_free), ptr(left), to_int("B", B),
-                            page, to_int("max_pages", table.size(1)), to_int("capacity", free_pages.size(0)), pages,
-                            current_stream(dev)),
-         "attn_page_release");
+    call("attn_page_release", [&] {
+        return calls.page_release(ptr(seqlens), ptr(keep_lens), ptr(table), ptr(free_pages), ptr(n_free), ptr(left), to_int("B", B),
+                                  page, to_int("max_pages", table.size(1)), to_int("capacity", free_pages.size(0)), pages,
+                                  current_stream(dev));
+    });
     return left;
 }
 
@@ -201,12 +210,13 @@ Tensor rope_append(const Tensor& q, const Tensor& k, const Tensor& v, const Tens
     TORCH_CHECK_VALUE(static_cast<int64_t>(sections.size()) == n_axes, n_axes, " position axes need as many sections, got ", sections.size());
     const c10::cuda::CUDAGuard guard(dev);
     Tensor out = result("out", out_, at::kBFloat16, {B, Hq, L, D}, dev);
-    done(calls.rope_append(ptr<void>(q), ptr<void>(k), ptr<void>(v), qs, ks, vs, ptr(positions), ptr<float>(inv_freq), ptr(slots),
-                           ptr<void>(out), ptr<void>(k_cache), ptr<void>(v_cache), ptr<void>(k_scale), ptr<void>(v_scale), fmt,
-                           to_int("B", B), to_int("L", L), to_int("Hq", Hq), to_int("Hkv", Hkv), to_int("D", D), to_int("rot", rot),
-                           to_int("n", n_outer), to_int("rows", rows), to_int("n_axes", n_axes), sections.data(), cycle, adjacent,
-                           current_stream(dev)),
-         "attn_rope_append");
+    call("attn_rope_append", [&] {
+        return calls.rope_append(ptr<void>(q), ptr<void>(k), ptr<void>(v), qs, ks, vs, ptr(positions), ptr<float>(inv_freq), ptr(slots),
+                                 ptr<void>(out), ptr<void>(k_cache), ptr<void>(v_cache), ptr<void>(k_scale), ptr<void>(v_scale), fmt,
+                                 to_int("B", B), to_int("L", L), to_int("Hq", Hq), to_int("Hkv", Hkv), to_int("D", D), to_int("rot", rot),
+                                 to_int("n", n_outer), to_int("rows", rows), to_int("n_axes", n_axes), sections.data(), cycle, adjacent,
+                                 current_stream(dev));
+    });
     return out;
 }
 
@@ -256,14 +266,16 @@ std::tuple<Tensor, Maybe> decode_tree(const Tensor& q, const Tensor& k, const Te
     }
     const uint32_t* words = ptr<uint32_t>(mask);
     if (table)
-        done(calls.decode_tree_paged(ptr<void>(q), ptr<void>(k), ptr<void>(v), ptr(*table), ptr(seqlens), words, per_seq, ptr(tree_lens),
-                                     ptr<void>(out), ptr<float>(lse), b, hq, hkv, t, n_outer, rows, max_pages, d, scale,
-                                     ptr<void>(workspace), bytes, current_stream(dev)),
-             "attn_decode_tree_paged");
+        call("attn_decode_tree_paged", [&] {
+            return calls.decode_tree_paged(ptr<void>(q), ptr<void>(k), ptr<void>(v), ptr(*table), ptr(seqlens), words, per_seq, ptr(tree_lens),
+                                           ptr<void>(out), ptr<float>(lse), b, hq, hkv, t, n_outer, rows, max_pages, d, scale,
+                                           ptr<void>(workspace), bytes, current_stream(dev));
+        });
     else
-        done(calls.decode_tree(ptr<void>(q), ptr<void>(k), ptr<void>(v), ptr(seqlens), words, per_seq, ptr(tree_lens), ptr<void>(out),
-                               ptr<float>(lse), b, hq, hkv, t, rows, d, scale, ptr<void>(workspace), bytes, current_stream(dev)),
-             "attn_decode_tree");
+        call("attn_decode_tree", [&] {
+            return calls.decode_tree(ptr<void>(q), ptr<void>(k), ptr<void>(v), ptr(seqlens), words, per_seq, ptr(tree_lens), ptr<void>(out),
+                                     ptr<float>(lse), b, hq, hkv, t, rows, d, scale, ptr<void>(workspace), bytes, current_stream(dev));
+        });
     return {out, lse};
 }
 
@@ -287,11 +299,12 @@ Tensor tree_commit(const Tensor& k, const Tensor& v, const Tensor& seqlens, cons
                       "shape mismatch between seqlens, the caches, block_table and tree_lens");
     const c10::cuda::CUDAGuard guard(dev);
     Tensor out = result("out_seqlens", out_seqlens_, at::kInt, {B}, dev);
-    done(calls.tree_commit(ptr<void>(k), ptr<void>(v), ptr(table), ptr(seqlens), ptr(tree_lens), ptr(accept), ptr(n_accept), ptr(out),
-                           to_int("B", B), to_int("Hkv", k.size(1)), t, to_int("A", accept.size(1)), to_int("D", k.size(3)),
-                           to_int("n", k.size(0)), to_int("rows", k.size(2)), table ? to_int("max_pages", table->size(1)) : 0,
-                           current_stream(dev)),
-         "attn_tree_commit");
+    call("attn_tree_commit", [&] {
+        return calls.tree_commit(ptr<void>(k), ptr<void>(v), ptr(table), ptr(seqlens), ptr(tree_lens), ptr(accept), ptr(n_accept), ptr(out),
+                                 to_int("B", B), to_int("Hkv", k.size(1)), t, to_int("A", accept.size(1)), to_int("D", k.size(3)),
+                                 to_int("n", k.size(0)), to_int("rows", k.size(2)), table ? to_int("max_pages", table->size(1)) : 0,
+                                 current_stream(dev));
+    });
     return out;
 }
 

@@ -66,6 +66,7 @@ def _plan_inputs(B, L, page, max_pages, seed, spare):
 @pytest.mark.parametrize("B,L,page,max_pages,spare", [
     (1, 1, 64, 1, 0), (1, 1, 64, 3, 1), (3, 5, 64, 4, 2), (64, 1, 64, 9, 7), (33, 100, 1, 130, 900), (200, 700, 128, 12, 500),
     (1024, 9, 64, 3, 300), (1025, 3, 64, 2, 100), (2500, 2, 256, 2, 1000), (4, 0, 64, 4, 3), (0, 4, 64, 2, 3),
+    (5, 3000, 64, 60, 150), (1, 9000, 128, 80, 100), (130, 63, 64, 5, 200),
 ])
 def test_page_plan(B, L, page, max_pages, spare, in_place):
     lens, new, table, free, n_free, n_pages = _plan_inputs(B, L, page, max_pages, B + L + page, spare)
@@ -158,6 +159,9 @@ def _on_gpu(t):
     (1, 1, 1, 1, 64, 64, 1, 0, 0, "e4m3"), (2, 31, 16, 4, 128, 96, 2, 0, 1, "e4m3"), (3, 5, 7, 7, 64, 32, 3, 1, 0, "e4m3"),
     (1, 1, 1, 1, 64, 64, 1, 0, 0, "q8_0"), (2, 31, 16, 4, 128, 96, 2, 0, 1, "q8_0"), (3, 5, 7, 7, 64, 48, 3, 1, 0, "q8_0"),
     (4, 16, 12, 3, 128, 128, 4, 0, 0, "q8_0"), (1, 300, 33, 17, 64, 64, 1, 0, 1, "q8_0"),
+    # many tokens: several a CTA, the last one with fewer
+    (1, 4737, 2, 1, 64, 64, 2, 1, 0, "bf16"), (3, 1603, 3, 2, 128, 96, 1, 0, 1, "e4m3"), (2, 2503, 1, 3, 128, 128, 3, 0, 0, "q8_0"),
+    (1, 5001, 1, 1, 256, 64, 4, 0, 1, "bf16"),
 ])
 @pytest.mark.parametrize("strided", [True, False])
 def test_rope_append(B, L, Hq, Hkv, D, rot, axes, cycle, adjacent, fmt, strided):
