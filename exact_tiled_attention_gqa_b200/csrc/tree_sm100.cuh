@@ -179,7 +179,7 @@ struct TreeCfg {
     static constexpr int kTileBytes = kTile * D * 2;
     // as many tiles as fit beside Q when kCtasPerSm CTAs share the SM's 228 KB (1 KB reserved per
     // CTA, 1 KB alignment slack, 1 KB for what follows the ring), at most 16
-    static constexpr int kStagesFit = (233472 / kCtasPerSm - 3072 - kQBytes) / kTileBytes;
+    static constexpr int kStagesFit = (233472 / kCtasPerSm - 3 * 1024 - kQBytes) / kTileBytes;
     static constexpr int kStages = kStagesFit > 16 ? 16 : kStagesFit;
     static constexpr int kKVOff = kQBytes;
     static constexpr int kBarOff = kKVOff + kStages * kTileBytes;

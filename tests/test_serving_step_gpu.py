@@ -225,6 +225,46 @@ def test_rope_append(B, L, Hq, Hkv, D, rot, axes, cycle, adjacent, fmt, strided)
         assert torch.equal(old, new)          # rows no token has are left as they were
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "q8_0"])
+def test_stored_codes_are_the_quotients_to_nearest(fmt):
+    """V's codes, which no rotation precedes, are those of the division itself, to the last one: every bf16 value of
+    64K bit patterns but NaN over scales with ties among the quotients, and scales at the ends of float32."""
+    D, Hkv = 128, 8
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    bits = torch.where(bits.isnan(), torch.zeros_like(bits), bits)
+    g = torch.Generator().manual_seed(0)
+    if fmt == "q8_0":
+        bits = torch.where(bits.isinf() | (bits.abs() > 8e6), torch.ones_like(bits), bits)
+        bits = bits[torch.randperm(1 << 16, generator=g)] * torch.exp2(torch.randint(-30, 3, (1 << 11, 1), generator=g).float()).to(
+            torch.bfloat16).expand(-1, 32).reshape(-1)
+        bits = torch.where(bits.abs() > 8e6, torch.ones_like(bits), bits)
+    L = (1 << 16) // D
+    v = bits.view(1, L, 1, D).expand(1, L, Hkv, D).contiguous()
+    slots = torch.arange(L).int().view(1, L)
+    n_pages = -(-L // 64)
+    inv, pos = torch.zeros(0), torch.zeros(1, L, dtype=torch.int32)
+    args = [t.cuda() for t in (v, v, v, pos, inv, slots)]
+    if fmt == "e4m3":
+        scale = torch.tensor([1.0, 0.75, 0.1, 3.0, 1e-3, 1.7e-38, 3e38, 2.0 ** -40])
+        kc, vc = (torch.zeros(n_pages, Hkv, 64, D, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+        attn.rope_append(*args, kc, vc, k_scale=scale.cuda(), v_scale=scale.cuda())
+        want = (v.float() / scale[None, None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        for c in (kc, vc):
+            got = c.cpu().transpose(1, 2).flatten(0, 1)[:L]
+            assert torch.equal(got.view(torch.int8), want[0].view(torch.int8))
+    else:
+        kc, vc = (torch.zeros(n_pages, Hkv, 64, D, dtype=torch.int8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(n_pages, Hkv, 64, D // 32, dtype=torch.float16, device="cuda") for _ in range(2))
+        attn.rope_append(*args, kc, vc, k_scale=ks, v_scale=vs)
+        x = v[0].float().unflatten(-1, (-1, 32))
+        d = (x.abs().amax(-1) / 127).half()
+        want = torch.where(d[..., None] > 0, (x / d[..., None].float()).round().clamp(-127, 127), torch.zeros_like(x)).to(torch.int8)
+        for c, sc in ((kc, ks), (vc, vs)):
+            assert torch.equal(sc.cpu().transpose(1, 2).flatten(0, 1)[:L], d)
+            assert torch.equal(c.cpu().transpose(1, 2).flatten(0, 1)[:L], want.flatten(-2))
+    assert attn.device_error(reset=True) == 0
+
+
 def test_rope_far_positions_and_special_values():
     """Angles at the ends of int32 hold to 3e-6 rad (2^31 2^-52 f turns more than near ones); infinities and NaN come
     through; a contiguous cache is a pool of B slabs; a slot past the cache is flagged and not written."""
