@@ -192,8 +192,8 @@ int check_plan(const PlanParams& p) {
     if (static_cast<long long>(p.n_pages) * p.page_size > 0x7fffffffLL)
         return fail(ATTN_ERR_UNSUPPORTED, "n_pages * page_size too large for 32-bit slots");
     if (static_cast<long long>(p.max_pages) * p.page_size > 0x7fffffffLL ||
-        static_cast<long long>(p.B) * p.max_pages > 0x3fffffffLL || p.capacity > 0x3fffffff)
-        return fail(ATTN_ERR_UNSUPPORTED, "block table or page stack too large");
+        static_cast<long long>(p.B) * p.max_pages > 0x3fffffffLL || p.capacity > 0x3fffffff || p.L > 0x3fffffff)
+        return fail(ATTN_ERR_UNSUPPORTED, "block table, page stack or L too large");
     return ATTN_OK;
 }
 // attn_page_plan_kernel writes up to this many slots itself, a second kernel on the whole GPU more.  Device time
@@ -384,6 +384,7 @@ extern "C" int attn_tree_commit(void* k_cache, void* v_cache, const int32_t* blo
     if (B < 0 || Hkv < 1 || T < 1 || A < 0) return fail(ATTN_ERR_INVALID_ARG, "bad size (B=%d Hkv=%d T=%d A=%d)", B, Hkv, T, A);
     if (D != 64 && D != 128 && D != 256) return fail(ATTN_ERR_UNSUPPORTED, "head dim D=%d (built: 64, 128, 256)", D);
     if (T > kTreeMaxNodes) return fail(ATTN_ERR_UNSUPPORTED, "T=%d nodes (built: up to %d)", T, kTreeMaxNodes);
+    if (Hkv > 0xffffff) return fail(ATTN_ERR_UNSUPPORTED, "too many heads (Hkv=%d)", Hkv);
     if (n_outer < 0 || page_size < 1 || (block_table && (n_outer < 1 || max_pages < 1)) || (!block_table && n_outer < B))
         return fail(ATTN_ERR_INVALID_ARG, "bad cache size (outer=%d rows=%d max_pages=%d)", n_outer, page_size, max_pages);
     if (block_table && static_cast<long long>(page_size) * max_pages > 0x7fffffffLL)

@@ -584,8 +584,8 @@ int attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pag
  * above L or a length above max_pages * page_size refuses the request and flags
  * ATTN_DEVERR_SEQLEN; an n_free outside [0, capacity] is clamped and flags
  * ATTN_DEVERR_PAGE, as does a page outside [0, n_pages), whose slots are -1.
- * Limits: n_pages * page_size and max_pages * page_size below 2^31, B * max_pages
- * and capacity below 2^30.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
+ * Limits: n_pages * page_size and max_pages * page_size below 2^31, B * max_pages,
+ * capacity and L below 2^30.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
  * ATTN_ERR_CUDA.
  */
 int attn_page_plan(const int32_t* seqlens, const int32_t* new_lens, int32_t* block_table, const int32_t* free_pages,
@@ -677,7 +677,7 @@ int attn_rope_append(const void* q, const void* k, const void* v, long long q_st
  * A length or a path that cannot be moves nothing, leaves the length as it is
  * and flags ATTN_DEVERR_SEQLEN or ATTN_DEVERR_INDEX; rows in a page outside the
  * pool are left out and flag ATTN_DEVERR_PAGE.  D: 64, 128 or 256.  T: 1 .. 1024.
- * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ * Hkv: below 2^24.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
  */
 int attn_tree_commit(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seqlens,
                      const int32_t* tree_lens, const int32_t* accept, const int32_t* n_accept, int32_t* out_seqlens,

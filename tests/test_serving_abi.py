@@ -208,3 +208,14 @@ def test_sizes_are_refused_with_words(lib):
         attn.page_release(z(2), z(2), z(2, 4), z(8), z(1), page_size=-64, n_pages=8)
     with pytest.raises(ValueError, match="T=-2"):
         attn.tree_commit(bf, bf, z(1), z(1, 2), z(1), T=-2)
+
+
+def test_sizes_past_32_bit_indexes_are_refused(lib):
+    """Rows of a step are counted in steps of up to 1024 past L, and a commit's 16-byte
+    columns as 2 * Hkv * D / 8, both in 32 bits."""
+    for L in (1 << 30, 2**31 - 1024, 2**31 - 1):
+        assert _call(lib.attn_page_plan, PLAN, dict(L=L)) == -2
+        assert b"too large" in lib.attn_last_error()
+    for Hkv in (1 << 24, 1 << 26, 2**31 - 1):
+        assert _call(lib.attn_tree_commit, COMMIT, dict(Hkv=Hkv, D=256)) == -2
+        assert b"heads" in lib.attn_last_error()
