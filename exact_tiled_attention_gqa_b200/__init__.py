@@ -620,16 +620,20 @@ def decode_tree_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
 def page_plan(seqlens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
               n_free: torch.Tensor, *, L: int, page_size: int, n_pages: int, slots: Optional[torch.Tensor] = None,
               out_seqlens: Optional[torch.Tensor] = None, out_n_free: Optional[torch.Tensor] = None,
-              status: Optional[torch.Tensor] = None, stream=None):
+              status: Optional[torch.Tensor] = None, granted: Optional[torch.Tensor] = None, stream=None):
     """Pages and cache slots for new_lens[b] <= L new rows of every request (all int32 on one CUDA device).
 
     seqlens, new_lens [B]; block_table [B,max_pages], written for the new pages; free_pages [capacity] with n_free
     [1] valid entries, popped from the top, requests in order.  A request the pages do not reach for, or the table
     has no room for, is refused: status 1, length as it was, slots -1.  Returns (slots [B,L], out_seqlens [B],
-    out_n_free [1], status [B]); out_seqlens may be seqlens and out_n_free n_free."""
+    out_n_free [1], status [B]); out_seqlens may be seqlens and out_n_free n_free.
+
+    granted [B] (may be new_lens), if given, is written: new_lens[b] where served, 0 where refused.  When the rows are
+    a tree's nodes, it is the tree_lens of decode_tree_paged and tree_commit: new_lens would make them take the last
+    committed rows of a refused request for its tree."""
     with _on(stream, seqlens):
         return _native.calls().page_plan(seqlens, new_lens, block_table, free_pages, n_free, L, page_size, n_pages, slots, out_seqlens,
-                                         out_n_free, status)
+                                         out_n_free, status, granted)
 
 
 def page_release(seqlens: torch.Tensor, keep_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -665,8 +669,9 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Ten
                 tree_lens: Optional[torch.Tensor] = None, out_seqlens: Optional[torch.Tensor] = None, stream=None):
     """Move the accepted path's K and V rows together after decode_tree.  Caches bf16 [B,Hkv,Lmax,D], or pools
     [n_pages,Hkv,page_size,D] with block_table int32 [B,max_pages]; seqlens int32 [B] with the tree's rows;
-    accept int32 [B,A] the path's nodes, increasing, the first n_accept[b] of them taken.  T, tree_lens as in
-    decode_tree.  Returns out_seqlens int32 [B] (may be seqlens): the rows before the tree plus n_accept."""
+    accept int32 [B,A] the path's nodes, increasing, the first n_accept[b] of them taken (none where the tree has no
+    nodes).  T, tree_lens as in decode_tree; after page_plan, tree_lens is its granted.  Returns out_seqlens int32 [B]
+    (may be seqlens): the rows before the tree plus n_accept."""
     with _on(stream, k_cache):
         return _native.calls().tree_commit(k_cache, v_cache, seqlens, accept, n_accept, T, block_table, tree_lens, out_seqlens)
 

@@ -74,6 +74,7 @@ SIGNATURES = {
     "attn_decode_tree_paged": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                       _i32, _i32, _i32, _f32, _vp, _sz, _vp]),
     "attn_page_plan": (_i32, [_vp] * 9 + [_i32] * 6 + [_vp]),
+    "attn_page_plan_granted": (_i32, [_vp] * 10 + [_i32] * 6 + [_vp]),
     "attn_page_release": (_i32, [_vp] * 6 + [_i32] * 5 + [_vp]),
     "attn_rope_append": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                                 _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), _i32, _i32, _vp]),
@@ -116,7 +117,7 @@ def lib() -> ctypes.CDLL:
 
 
 # the C functions csrc/torch_calls.cpp calls
-BOUND = ("attn_page_plan", "attn_page_release", "attn_rope_append", "attn_decode_tree", "attn_decode_tree_workspace_size",
+BOUND = ("attn_page_plan_granted", "attn_page_release", "attn_rope_append", "attn_decode_tree", "attn_decode_tree_workspace_size",
          "attn_decode_tree_paged", "attn_decode_tree_paged_workspace_size", "attn_tree_commit")
 
 _calls = None

@@ -187,7 +187,8 @@ int check_plan(const PlanParams& p) {
         return fail(ATTN_ERR_INVALID_ARG, "null free_pages, n_free or out_n_free");
     if (p.B > 0 && (!p.seqlens || !p.new_lens || !p.table)) return fail(ATTN_ERR_INVALID_ARG, "null lengths or block_table");
     if (!aligned4(p.seqlens) || !aligned4(p.new_lens) || !aligned4(p.table) || !aligned4(p.free_pages) ||
-        !aligned4(p.n_free) || !aligned4(p.slots) || !aligned4(p.out_seqlens) || !aligned4(p.out_n_free) || !aligned4(p.status))
+        !aligned4(p.n_free) || !aligned4(p.slots) || !aligned4(p.out_seqlens) || !aligned4(p.out_n_free) || !aligned4(p.status) ||
+        !aligned4(p.granted))
         return fail(ATTN_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
     if (static_cast<long long>(p.n_pages) * p.page_size > 0x7fffffffLL)
         return fail(ATTN_ERR_UNSUPPORTED, "n_pages * page_size too large for 32-bit slots");
@@ -232,8 +233,16 @@ extern "C" int attn_page_plan(const int32_t* seqlens, const int32_t* new_lens, i
                               const int32_t* free_pages, const int32_t* n_free, int32_t* slots, int32_t* out_seqlens,
                               int32_t* out_n_free, int32_t* status, int B, int L, int page_size, int max_pages,
                               int capacity, int n_pages, void* stream) {
+    return attn_page_plan_granted(seqlens, new_lens, block_table, free_pages, n_free, slots, out_seqlens, out_n_free, status,
+                                  nullptr, B, L, page_size, max_pages, capacity, n_pages, stream);
+}
+
+extern "C" int attn_page_plan_granted(const int32_t* seqlens, const int32_t* new_lens, int32_t* block_table,
+                                      const int32_t* free_pages, const int32_t* n_free, int32_t* slots,
+                                      int32_t* out_seqlens, int32_t* out_n_free, int32_t* status, int32_t* granted, int B,
+                                      int L, int page_size, int max_pages, int capacity, int n_pages, void* stream) {
     PlanParams p = {seqlens, new_lens, block_table, const_cast<int32_t*>(free_pages), n_free, slots, out_seqlens,
-                    out_n_free, status, B, L, page_size, max_pages, capacity, n_pages};
+                    out_n_free, status, granted, B, L, page_size, max_pages, capacity, n_pages};
     int st = check_plan(p);
     if (st != ATTN_OK) return st;
     if (B > 0 && (!out_seqlens || !status || (!slots && L > 0)))
@@ -259,7 +268,7 @@ extern "C" int attn_page_release(const int32_t* seqlens, const int32_t* keep_len
                                  int32_t* free_pages, const int32_t* n_free, int32_t* out_n_free, int B, int page_size,
                                  int max_pages, int capacity, int n_pages, void* stream) {
     PlanParams p = {seqlens, keep_lens, const_cast<int32_t*>(block_table), free_pages, n_free, nullptr, nullptr,
-                    out_n_free, nullptr, B, 0, page_size, max_pages, capacity, n_pages};
+                    out_n_free, nullptr, nullptr, B, 0, page_size, max_pages, capacity, n_pages};
     int st = check_plan(p);
     if (st != ATTN_OK) return st;
     st = launch_plan(attn_page_release_kernel, static_cast<long long>(B) * max_pages <= kReleaseEntries, static_cast<cudaStream_t>(stream), p,

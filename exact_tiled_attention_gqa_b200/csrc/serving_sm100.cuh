@@ -35,6 +35,7 @@ struct PlanParams {
     int* out_seqlens;        // [B]
     int* out_n_free;         // [1]
     int* status;             // [B]
+    int* granted;            // [B] or nullptr; may be new_lens
     int B, L, page_size, max_pages, capacity, n_pages;
 };
 
@@ -126,7 +127,8 @@ __device__ __forceinline__ void plan_copy_runs(const int* lo, const int* hi, int
 // The scan, the table's new entries, the lengths and, with SLOTS, the slots; requests in
 // chunks of the block.  One CTA, or a cluster of kPlanCluster CTAs that all scan (the
 // lengths are few) and share the copies.  Every CTA has read a chunk's lengths, and n_free,
-// before any writes that chunk's outputs, so out_seqlens may be seqlens and out_n_free n_free.
+// before any writes that chunk's outputs, so out_seqlens may be seqlens, granted new_lens and
+// out_n_free n_free.
 template <bool SLOTS>
 __global__ void __launch_bounds__(kPlanThreads) attn_page_plan_kernel(const PlanParams p) {
     grid_dep_release();
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_page_plan_kernel(const Plan
         if (rank == 0 && b < p.B) {
             p.out_seqlens[b] = served ? have + want : have;
             p.status[b] = served ? 0 : 1;
+            if (p.granted != nullptr) p.granted[b] = served ? want : 0;
         }
         auto popped = [&](int i, int c) { return __ldg(p.free_pages + (n_free - 1 - (s_first[i] + c - s_used[i]))); };
         plan_copy_runs(
@@ -202,7 +205,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_page_plan_kernel(const Plan
 }
 
 // The slot of every new row, from the table and lengths attn_page_plan_kernel wrote: units of
-// kSlotRun rows of one request.
+// kSlotRun rows of one request.  (new_lens may be `granted` by now: the same where a request was
+// served.)
 constexpr int kSlotThreads = 256;
 constexpr int kSlotRun = 4 * kSlotThreads;
 
@@ -558,7 +562,7 @@ __global__ void __launch_bounds__(kCommitThreads) attn_tree_commit_kernel(const 
     const int b = blockIdx.x;
     const int seqlen = p.seqlens[b];
     const int n_b = p.tree_lens != nullptr ? p.tree_lens[b] : p.T;
-    const int n = p.n_accept[b];
+    const int n = n_b == 0 ? 0 : p.n_accept[b];        // no tree (its rows were refused, say): nothing to accept
     const int* path = p.accept + static_cast<size_t>(b) * p.A;
     const long long cap = p.table != nullptr ? static_cast<long long>(p.max_pages) * p.page_size : p.page_size;
     unsigned int err = 0u;

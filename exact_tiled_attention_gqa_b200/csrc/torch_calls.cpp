@@ -26,7 +26,7 @@ using Maybe = std::optional<Tensor>;
 namespace {
 
 struct Calls {
-    decltype(&attn_page_plan) page_plan = nullptr;
+    decltype(&attn_page_plan_granted) page_plan = nullptr;
     decltype(&attn_page_release) page_release = nullptr;
     decltype(&attn_rope_append) rope_append = nullptr;
     decltype(&attn_decode_tree) decode_tree = nullptr;
@@ -42,7 +42,7 @@ void bind(const py::dict& addresses, const py::object& check) {
     auto get = [&](auto& fn, const char* name) {
         fn = reinterpret_cast<std::decay_t<decltype(fn)>>(py::cast<uintptr_t>(addresses[name]));
     };
-    get(calls.page_plan, "attn_page_plan");
+    get(calls.page_plan, "attn_page_plan_granted");
     get(calls.page_release, "attn_page_release");
     get(calls.rope_append, "attn_rope_append");
     get(calls.decode_tree, "attn_decode_tree");
@@ -123,16 +123,17 @@ int64_t check_pages(const Tensor& seqlens, const Tensor& lens, const char* lens_
 std::tuple<Tensor, Tensor, Tensor, Tensor> page_plan(const Tensor& seqlens, const Tensor& new_lens, const Tensor& table,
                                                      const Tensor& free_pages, const Tensor& n_free, int64_t L, int64_t page_size,
                                                      int64_t n_pages, const Maybe& slots_, const Maybe& out_seqlens_,
-                                                     const Maybe& out_n_free_, const Maybe& status_) {
+                                                     const Maybe& out_n_free_, const Maybe& status_, const Maybe& granted) {
     const int l = to_int("L", L), page = to_int("page_size", page_size), pages = to_int("n_pages", n_pages);
     const int64_t B = check_pages(seqlens, new_lens, "new_lens", table, free_pages, n_free);
     const c10::Device dev = seqlens.device();
     const c10::cuda::CUDAGuard guard(dev);
+    if (granted) result("granted", granted, at::kInt, {B}, dev);
     Tensor slots = result("slots", slots_, at::kInt, {B, L}, dev), lens = result("out_seqlens", out_seqlens_, at::kInt, {B}, dev);
     Tensor left = result("out_n_free", out_n_free_, at::kInt, {1}, dev), status = result("status", status_, at::kInt, {B}, dev);
     call("attn_page_plan", [&] {
         return calls.page_plan(ptr(seqlens), ptr(new_lens), ptr(table), ptr(free_pages), ptr(n_free), ptr(slots), ptr(lens), ptr(left),
-                               ptr(status), to_int("B", B), l, page, to_int("max_pages", table.size(1)),
+                               ptr(status), ptr(granted), to_int("B", B), l, page, to_int("max_pages", table.size(1)),
                                to_int("capacity", free_pages.size(0)), pages, current_stream(dev));
     });
     return {slots, lens, left, status};

@@ -526,7 +526,8 @@ int attn_decode_kv8_paged(const void* q, const void* k_pages, const void* v_page
  *   tree_mask  [B, T, W] or [T, W]  uint32, read; W = (T + 31) / 32; [T, W] (one mask for
  *                                   every sequence) when mask_per_seq == 0
  *   tree_lens  [B] or NULL          int32 in device memory, each in [0, T]; a value outside
- *                                   is clamped and flags ATTN_DEVERR_INDEX
+ *                                   is clamped and flags ATTN_DEVERR_INDEX.  Where rows may
+ *                                   be refused: `granted` of attn_page_plan_granted
  *   out        [B, Hq, T, D]        bf16, written
  *   lse        [B, Hq, T]           fp32, written; may be NULL
  *   workspace  attn_decode_tree_workspace_size(...) bytes, 256-byte aligned, as attn_decode
@@ -556,8 +557,8 @@ int attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pag
                            void* stream);
 
 /*
- * attn_page_plan -- the pages and cache slots of a step's new rows, from the
- * requests' lengths: block tables and slot maps without the host.
+ * attn_page_plan / attn_page_plan_granted -- the pages and cache slots of a step's new
+ * rows, from the requests' lengths: block tables and slot maps without the host.
  *
  * Request b has seqlens[b] rows and gets new_lens[b] more.  It holds
  * ceil(seqlens[b] / page_size) pages, in block_table[b]; the new ones it needs
@@ -579,6 +580,13 @@ int attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pag
  *                               was).  May be seqlens.
  *   out_n_free  [1]             int32, written: pages left.  May be n_free.
  *   status      [B]             int32, written: 0 served, 1 refused
+ *   granted     [B] or NULL     int32, written: new_lens[b] of a served request, 0 of a refused
+ *                               one.  May be new_lens.  (attn_page_plan: NULL)
+ *
+ * A refused request has none of its new rows.  A call that is told how many of a
+ * request's last rows are new (tree_lens of attn_decode_tree_paged and attn_tree_commit)
+ * must be told `granted`: new_lens there would make the last committed rows of a refused
+ * request its tree.
  *
  * Other overlaps of the arrays are not allowed.  A length below 0, a new length
  * above L or a length above max_pages * page_size refuses the request and flags
@@ -591,6 +599,10 @@ int attn_decode_tree_paged(const void* q, const void* k_pages, const void* v_pag
 int attn_page_plan(const int32_t* seqlens, const int32_t* new_lens, int32_t* block_table, const int32_t* free_pages,
                    const int32_t* n_free, int32_t* slots, int32_t* out_seqlens, int32_t* out_n_free, int32_t* status,
                    int B, int L, int page_size, int max_pages, int capacity, int n_pages, void* stream);
+int attn_page_plan_granted(const int32_t* seqlens, const int32_t* new_lens, int32_t* block_table,
+                           const int32_t* free_pages, const int32_t* n_free, int32_t* slots, int32_t* out_seqlens,
+                           int32_t* out_n_free, int32_t* status, int32_t* granted, int B, int L, int page_size,
+                           int max_pages, int capacity, int n_pages, void* stream);
 
 /*
  * attn_page_release -- the inverse: request b keeps its first keep_lens[b] of
@@ -671,7 +683,8 @@ int attn_rope_append(const void* q, const void* k, const void* v, long long q_st
  *                 share the pages of their tree rows.
  *   seqlens, tree_lens (or NULL: T)  as attn_decode_tree
  *   accept      [B, A]   int32, read
- *   n_accept    [B]      int32, read; in [0, min(A, n_b)]
+ *   n_accept    [B]      int32, read; in [0, min(A, n_b)]; not read where n_b is 0 (a sequence
+ *                        without a tree accepts nothing and keeps its length)
  *   out_seqlens [B]      int32, written; may be seqlens
  *
  * A length or a path that cannot be moves nothing, leaves the length as it is
