@@ -14,7 +14,7 @@ namespace attn {
 // ---------------------------------------------------------------------------
 // page_plan / page_release: bound by the launch and a few round trips to memory (64
 // requests, one row each: 4.2 us on the device; 512 prompts of up to 4096 rows, 8.5 MB
-// of slots: 11.2 us in two launches; release of 512 requests' 33K pages: 8.0 us).
+// of slots: 11.2 us in two launches; release of 512 requests' 33K pages: 7.5 us).
 //
 // Request b has s_b rows and gets n_b more; with pages of P rows it holds
 // u_b = ceil(s_b / P) pages and needs ceil((s_b + n_b) / P) - u_b new ones.
@@ -86,6 +86,22 @@ __device__ __forceinline__ void plan_sync() {
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
+}
+
+// Whether any thread of the launch's CTAs says so, for the threads of CTA 0, after all CTAs' writes; the
+// others come back at once, for their end.  `flag` of CTA 0 is 0 since before an earlier plan_sync.
+__device__ __forceinline__ bool plan_any(bool mine, int* flag) {
+    if (gridDim.x == 1) return __syncthreads_or(mine) != 0;
+    if (mine) {
+        uint32_t first;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first) : "r"(smem_u32(flag)));
+        asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(first) : "memory");
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (blockIdx.x != 0) return false;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return *static_cast<volatile int*>(flag) != 0;
 }
 
 // One warp's share of a copy of runs: entries lo[i] .. hi[i] - 1 of request i for
@@ -242,26 +258,32 @@ __global__ void __launch_bounds__(kSlotThreads) attn_page_slots_kernel(const Pla
     }
 }
 
+// Pages a request holds and keeps; none where the lengths cannot be.
+__device__ __forceinline__ bool release_pages(const PlanParams& p, int b, int& used, int& kept) {
+    const int have = p.seqlens[b], keep = p.new_lens[b];
+    used = kept = 0;
+    if (have < 0 || keep < 0 || keep > have || have > static_cast<long long>(p.max_pages) * p.page_size) return false;
+    used = pages_of(have, p.page_size);
+    kept = pages_of(keep, p.page_size);
+    return true;
+}
+
 // Pages past the rows a request keeps go back on the stack, requests and pages in order.
-// One CTA or a cluster, as attn_page_plan_kernel.
+// One CTA or a cluster, as attn_page_plan_kernel.  A page's place is the count of those before
+// it, good or bad; where a bad one turns up (an entry outside the pool, which must not be handed
+// out again), one warp writes the stack anew without them.
 __global__ void __launch_bounds__(kPlanThreads) attn_page_release_kernel(const PlanParams p) {
     __shared__ long long warp_sums[32];
-    __shared__ int s_used[kPlanThreads], s_kept[kPlanThreads], s_first[kPlanThreads];
+    __shared__ int s_used[kPlanThreads], s_kept[kPlanThreads], s_first[kPlanThreads], s_bad;
+    if (threadIdx.x == 0) s_bad = 0;
     const int n_free = plan_n_free(p);
     const int rank = blockIdx.x, n_cta = gridDim.x;
     long long before = n_free;
+    bool bad = false;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
         int used = 0, kept = 0;
-        if (b < p.B) {
-            const int have = p.seqlens[b], keep = p.new_lens[b];
-            if (have < 0 || keep < 0 || keep > have || have > static_cast<long long>(p.max_pages) * p.page_size) {
-                atomicOr(&g_attn_err, kDevErrSeqlen);
-            } else {
-                used = pages_of(have, p.page_size);
-                kept = pages_of(keep, p.page_size);
-            }
-        }
+        if (b < p.B && !release_pages(p, b, used, kept)) atomicOr(&g_attn_err, kDevErrSeqlen);
         long long gone;
         const long long first = before + block_scan(used - kept, warp_sums, gone);
         s_used[threadIdx.x] = used;
@@ -273,16 +295,35 @@ __global__ void __launch_bounds__(kPlanThreads) attn_page_release_kernel(const P
             min(kPlanThreads, p.B - b0),
             [&](int i, int c) { return __ldg(p.table + static_cast<size_t>(b0 + i) * p.max_pages + c); },
             [&](int i, int c, int page) {
-                if (page < 0 || page >= p.n_pages) atomicOr(&g_attn_err, kDevErrPage);
+                bad |= page < 0 || page >= p.n_pages;
                 const long long at = static_cast<long long>(s_first[i]) + c - s_kept[i];
                 if (at < p.capacity) p.free_pages[at] = page;
             });
         before += gone;
     }
-    if (rank == 0 && threadIdx.x == 0) {
-        if (before > p.capacity) atomicOr(&g_attn_err, kDevErrPage);
-        *p.out_n_free = static_cast<int>(min(before, static_cast<long long>(p.capacity)));
+    if (rank == 0 && threadIdx.x == 0) *p.out_n_free = static_cast<int>(min(before, static_cast<long long>(p.capacity)));
+    bad = plan_any(bad, &s_bad);
+    if (rank != 0) return;
+    if (bad && threadIdx.x < 32) {
+        before = n_free;
+        for (int b = 0; b < p.B; ++b) {
+            int used, kept;
+            release_pages(p, b, used, kept);
+            for (int c = kept + static_cast<int>(threadIdx.x); __any_sync(0xffffffffu, c < used); c += 32) {
+                const int page = c < used ? __ldg(p.table + static_cast<size_t>(b) * p.max_pages + c) : -1;
+                const bool good = page >= 0 && page < p.n_pages;
+                const unsigned int goods = __ballot_sync(0xffffffffu, good);
+                const long long at = before + __popc(goods & ((1u << threadIdx.x) - 1u));
+                if (good && at < p.capacity) p.free_pages[at] = page;
+                before += __popc(goods);
+            }
+        }
+        if (threadIdx.x == 0) {
+            atomicOr(&g_attn_err, kDevErrPage);
+            *p.out_n_free = static_cast<int>(min(before, static_cast<long long>(p.capacity)));
+        }
     }
+    if (threadIdx.x == 0 && before > p.capacity) atomicOr(&g_attn_err, kDevErrPage);
 }
 
 // ---------------------------------------------------------------------------

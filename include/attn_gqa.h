@@ -612,12 +612,12 @@ int attn_page_plan_granted(const int32_t* seqlens, const int32_t* new_lens, int3
  *   seqlens, keep_lens [B]  int32, read; 0 <= keep_lens[b] <= seqlens[b]; a pair that is
  *                           not releases nothing and flags ATTN_DEVERR_SEQLEN
  *   block_table             read (entries are left as they are)
- *   free_pages [capacity]   int32, written from n_free on
+ *   free_pages [capacity]   int32, written from n_free on (behind out_n_free with any value)
  *   n_free, out_n_free [1]  int32, read / written; may be the same
  *
- * Pages that would pass the stack's capacity are dropped and flag
- * ATTN_DEVERR_PAGE; an entry outside [0, n_pages) flags it too (and is put on
- * the stack as it is).  Limits and errors as attn_page_plan.
+ * An entry outside [0, n_pages) is left out, and pages that would pass the
+ * stack's capacity are dropped; both flag ATTN_DEVERR_PAGE.  Limits and errors
+ * as attn_page_plan.
  */
 int attn_page_release(const int32_t* seqlens, const int32_t* keep_lens, const int32_t* block_table,
                       int32_t* free_pages, const int32_t* n_free, int32_t* out_n_free, int B, int page_size,
