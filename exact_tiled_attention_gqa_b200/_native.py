@@ -131,7 +131,8 @@ def calls():
         with _lock:
             if _calls is None:
                 if not os.path.exists(CALLS_PATH):
-                    raise RuntimeError(f"{CALLS_PATH} is missing: build it with `python -m exact_tiled_attention_gqa_b200.build`")
+                    raise RuntimeError(f"{CALLS_PATH}, the binding for this Python and torch, is missing: "
+                                       "build it with `python -m exact_tiled_attention_gqa_b200.build`")
                 spec = importlib.util.spec_from_file_location(__package__ + "._torch_calls", CALLS_PATH)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)

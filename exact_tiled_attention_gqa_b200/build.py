@@ -18,6 +18,8 @@ import subprocess
 import sys
 import sysconfig
 
+import torch
+
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -27,8 +29,16 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 # unit mapping, ring positions, TMA coordinates and output indices and report a
 # violation as ATTN_DEVERR_BOUNDS (a checking build for tests, not for speed).
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libattn_gqa_sm100_debug_bounds.so")
-# the C++ binding of the serving-step calls, an importable module
-CALLS_PATH = os.path.join(PKG_DIR, "_torch_calls.so")
+
+
+def calls_path() -> str:
+    """The C++ binding of the serving-step calls, an importable module: its name holds the Python and torch it was
+    built against, whose C++ interfaces it uses, so that another one never loads it."""
+    return os.path.join(PKG_DIR, f"_torch_calls.{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}"
+                                 f"-cxx11abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}.so")
+
+
+CALLS_PATH = calls_path()
 CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -123,7 +133,6 @@ def build_calls(force: bool = False) -> str:
     if not force and os.path.exists(CALLS_PATH) and \
             all(os.path.getmtime(s) <= os.path.getmtime(CALLS_PATH) for s in (CALLS_SOURCE, header)):
         return CALLS_PATH
-    import torch
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
     torch_dir = os.path.dirname(torch.__file__)
     include, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
