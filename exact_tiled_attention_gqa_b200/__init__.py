@@ -671,7 +671,10 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Ten
     [n_pages,Hkv,page_size,D] with block_table int32 [B,max_pages]; seqlens int32 [B] with the tree's rows;
     accept int32 [B,A] the path's nodes, increasing, the first n_accept[b] of them taken (none where the tree has no
     nodes).  T, tree_lens as in decode_tree; after page_plan, tree_lens is its granted.  Returns out_seqlens int32 [B]
-    (may be seqlens): the rows before the tree plus n_accept."""
+    (may be seqlens): the rows before the tree plus n_accept.
+
+    A model of several layers calls this once a layer, each time with the lengths that still hold the tree's rows: let
+    out_seqlens be another tensor than seqlens (or seqlens in the last layer's call only)."""
     with _on(stream, k_cache):
         return _native.calls().tree_commit(k_cache, v_cache, seqlens, accept, n_accept, T, block_table, tree_lens, out_seqlens)
 

@@ -685,7 +685,9 @@ int attn_rope_append(const void* q, const void* k, const void* v, long long q_st
  *   accept      [B, A]   int32, read
  *   n_accept    [B]      int32, read; in [0, min(A, n_b)]; not read where n_b is 0 (a sequence
  *                        without a tree accepts nothing and keeps its length)
- *   out_seqlens [B]      int32, written; may be seqlens
+ *   out_seqlens [B]      int32, written; may be seqlens, but not before the last layer's call:
+ *                        every layer's cache moves by the lengths that still hold the tree,
+ *                        and shortened ones would move other rows, mostly unseen by the check
  *
  * A length or a path that cannot be moves nothing, leaves the length as it is
  * and flags ATTN_DEVERR_SEQLEN or ATTN_DEVERR_INDEX; rows in a page outside the
