@@ -205,8 +205,9 @@ constexpr long long kPlanSlots = 8192;
 // rows 4.5 and 4.9), the cluster of eight larger ones (512 of a row 5.0 us, on one CTA 5.3; 64 of 64 rows 5.0 and 6.7).
 constexpr int kPlanOneB = 128;
 constexpr long long kPlanOneSlots = 1024;
-// page_release does not know how many pages go: one CTA where the tables are small, the cluster where they could be
-// many (512 requests of up to 256 pages 15.6 us on one CTA and 8.0; 64 requests of a few pages 4.0 and 4.4).
+// page_release does not know how many pages go, only how many could: one CTA where the table is small, else the cluster
+// (512 requests of up to 256 pages 15.6 us on one CTA and 7.5).  A wide table of which little goes pays for the cluster:
+// 64 requests of up to 64 pages 4.1 us in a table of 64 columns, 4.3 in one of 512; of up to 16 pages 3.8 and 4.4.
 constexpr long long kReleaseEntries = 4096;
 
 int launch_plan(void (*kernel)(const PlanParams), bool one, cudaStream_t s, const PlanParams& p, const char* what) {
@@ -368,7 +369,6 @@ extern "C" int attn_rope_append(const void* q, const void* k, const void* v, lon
     p.L = L;
     p.Hq = Hq;
     p.Hkv = Hkv;
-    p.D = D;
     p.rot = rot;
     p.page_size = page_size;
     p.n_slots = static_cast<long long>(n_outer) * page_size;

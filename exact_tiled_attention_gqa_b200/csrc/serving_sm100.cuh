@@ -13,8 +13,8 @@ namespace attn {
 
 // ---------------------------------------------------------------------------
 // page_plan / page_release: bound by the launch and a few round trips to memory (64
-// requests, one row each: 4.2 us on the device; 512 prompts of up to 4096 rows, 8.5 MB
-// of slots: 11.2 us in two launches; release of 512 requests' 33K pages: 7.5 us).
+// requests, one row each: 4.0 us on the device; 512 prompts of up to 4096 rows, 8.5 MB
+// of slots: 10.9 us in two launches; release of 512 requests' 33K pages: 7.5 us).
 //
 // Request b has s_b rows and gets n_b more; with pages of P rows it holds
 // u_b = ceil(s_b / P) pages and needs ceil((s_b + n_b) / P) - u_b new ones.
@@ -353,7 +353,7 @@ struct RopeParams {
     __nv_bfloat16* q_out;               // [B, Hq, L, D]
     void *k_cache, *v_cache;            // [n_outer, Hkv, page_size, D]
     void *k_scale, *v_scale;            // E4M3: fp32 [Hkv]; q8_0: fp16 [n_outer, Hkv, page_size, D / 32]
-    int B, L, Hq, Hkv, D, rot, page_size;
+    int B, L, Hq, Hkv, rot, page_size;
     long long n_slots;                  // n_outer * page_size
     int n_axes, sections[4];
     int cycle;                          // axes taken in turn, not in blocks
@@ -400,8 +400,8 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 // 2i and 2i + 1).  A thread loads kRopeRows rows before it turns the first.
 //
 // Bound by the bytes of q, k and v in and q, K and V out, and by the issue of the turn
-// itself.  8192 tokens (32 + 8 heads of 128, E4M3 cache, 185 MB, 28.5 us at the copy rate):
-// one token a CTA and one row at a time 46.4 us; four tokens and two rows 41.1; the angles
+// itself.  8192 tokens, 5461 of them stored (32 + 8 heads of 128, E4M3 cache, 168 MB, 25.9 us at the
+// copy rate): one token a CTA and one row at a time 46.4 us; four tokens and two rows 41.1; the angles
 // laid out so that a row's reads of them meet no bank twice 37.1; no division per row 35.9;
 // eight tokens 35.5.  Four rows in flight at fewer CTAs 39.1, one row at more 35.9.
 template <int D, int FMT, bool ADJ, int TOK>
@@ -597,7 +597,7 @@ struct CommitParams {
 
 // One CTA per sequence (it alone reads and writes the sequence's length), a 16-byte column of
 // a head per thread, kCommitBatch rows in flight: bound by the round trips lengths -> path ->
-// pages -> rows (64 sequences, up to 9 rows of 8 heads of 128, paged: 6.1 us; 8 contiguous
+// pages -> rows (64 sequences, up to 9 rows of 8 heads of 128, paged: 5.9 us; 8 contiguous
 // ones, up to 5 rows: 2.8 us).
 __global__ void __launch_bounds__(kCommitThreads) attn_tree_commit_kernel(const CommitParams p) {
     const int b = blockIdx.x;

@@ -21,6 +21,12 @@
 // the others write a normalised partial (at most two a CTA) that a combine kernel merges.  The
 // loads run on across segments.
 //
+// P is rounded to bf16 for the MMA (its A operand has V's type, and two bf16 parts would double
+// P V); O is divided by the sum of the rounded P, so that a weight's rounding moves O by at most
+// 2^-8 of the weight times V's distance from O, and the log-sum-exp takes the unrounded sum.
+// Against 64 bits the bf16 result is off by 0.0021 (500 rows) to 0.0023 (1K to 32K) relative to
+// its norm; with weights in fp32 it would be 0.0017, the result's own rounding.
+//
 // Per tile of 64 cache rows S = Q K^T, P = 2^(S scale log2 e - m) and O += P V, with two S
 // buffers, so that S of the next tile is computed under the softmax of this one, as
 // attn_decode_tc_kernel.  D = 64 and 128: Q in shared memory, two CTAs on an SM.  D = 256: O
@@ -36,7 +42,8 @@
 // 32); what is left is the issuing warp going from one commit to the next wait.  Not faster: tiles
 // of 128 rows in two streams, each with a softmax warpgroup, on one CTA an SM (head dim 128, 770 us
 // for 683); looking for P and V half-way through Q K^T; waiting for K and V under P V (342K cycles
-// for 306K); head dim 256 with Q in shared memory (331K for 306K, with a shallower ring).
+// for 306K); head dim 256 with Q in shared memory (331K for 306K, with a shallower ring).  Tiles of
+// 128 rows at head dim 256 (O and two S fill the TMEM, Q back in shared memory) were not tried.
 //
 // The mask costs nothing over the committed rows: only a tile that reaches past c builds the
 // 64 visibility bits of its rows, each thread (one query row) shifting them out of its own
@@ -165,7 +172,7 @@ struct TreeCfg {
     static constexpr int kKB = D / 64;
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
     static constexpr bool kQTmem = D == 256;
-    static constexpr int kTile = 64;                          // cache rows of a tile
+    static constexpr int kTile = 64;                          // cache rows of a tile: the TMA boxes' (kDecKT), pages hold whole ones
     static constexpr int kThreads = 192;                      // softmax warps 0-3, producer, MMA issuer
     static constexpr int kProducerWarp = 4;
     static constexpr int kMmaWarp = 5;
@@ -411,16 +418,15 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                 }
                 __syncwarp();
             }
-            // Pages of the segment's 64-row boxes, a window of 32 in the warp's lanes and the next one
-            // on its way: looked up box by box they held the loads back (with two boxes a tile, 978 us for 869
-            // at 64 requests of 1K to 32K rows).
-            const int boxes_before = s.t0 * (kTile / 64), boxes_end = min(s.t1 * (kTile / 64), (s.seqlen + 63) / 64);
-            int window = boxes_before, here = 0, after = 0;
-            auto lookup = [&](int box0) {
-                const int i = box0 + lane;
-                if (p.block_table == nullptr || i >= boxes_end) return 0;
+            // Pages of the segment's tiles, a window of 32 in the warp's lanes and the next one on its way:
+            // looked up tile by tile they held the loads back (with tiles of 128 rows, 978 us for 869 at 64
+            // requests of 1K to 32K rows).
+            int window = s.t0, here = 0, after = 0;
+            auto lookup = [&](int tile0) {
+                const int i = tile0 + lane;
+                if (p.block_table == nullptr || i >= s.t1) return 0;
                 const int page = __ldg(p.block_table + static_cast<size_t>(s.b) * p.max_pages +
-                                       static_cast<int>(static_cast<long long>(i) * 64 / p.page_size));
+                                       static_cast<int>(static_cast<long long>(i) * kTile / p.page_size));
                 if (page >= 0 && page < p.n_pages) return page;
                 atomicOr(&g_attn_err, kDevErrPage);
                 return 0;
@@ -432,9 +438,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                 int j;
                 ring_tile<1>(i, n_tiles, is_v, j);
                 ATTN_CHECK(j >= 0 && j < n_tiles && s.b < p.B && s.g < p.Hkv);
-                const int box0 = boxes_before + j * (kTile / 64);
-                const int boxes = min(kTile / 64, boxes_end - box0);
-                if (is_v && box0 >= window + 32) {             // (K is at most two tiles ahead of V)
+                const int tile = s.t0 + j;
+                if (is_v && tile >= window + 32) {             // (K is at most two tiles ahead of V)
                     window += 32;
                     here = after;
                     after = lookup(window + 32);
@@ -443,25 +448,21 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, TreeCfg<D>::kCtasPerSm)
                 if (!ok) break;
                 if (lane == 0) {
                     if (ATTN_DEBUG_BOUNDS) ring_tag[at.e] = at.item;
-                    mbar_arrive_expect_tx(bar_full(at.e), static_cast<uint32_t>(boxes * 64 * D * 2));
+                    mbar_arrive_expect_tx(bar_full(at.e), static_cast<uint32_t>(L::kTileBytes));
                 }
                 const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-#pragma unroll
-                for (int h = 0; h < kTile / 64; ++h) {
-                    const int k = box0 + h - window;
-                    const int page = __shfl_sync(0xffffffffu, k < 32 ? here : after, k & 31);
-                    if (lane == 0 && h < boxes) {
-                        const int key = (box0 + h) * 64;
-                        int row = key, outer = s.b * p.Hkv + s.g;
-                        if (p.block_table != nullptr) {
-                            row = key % p.page_size;
-                            outer = page * p.Hkv + s.g;
-                        }
-                        decode_check_tile(p, row, outer);
-                        const uint32_t dst = sKV + at.e * L::kTileBytes + h * 64 * 128;
-                        for (int kb = 0; kb < L::kKB; ++kb)
-                            tma_load_3d(dst + kb * L::kBlockBytes, map, bar_full(at.e), kb * 64, row, outer);
+                const int k = tile - window;
+                const int page = __shfl_sync(0xffffffffu, k < 32 ? here : after, k & 31);
+                if (lane == 0) {
+                    int row = tile * kTile, outer = s.b * p.Hkv + s.g;
+                    if (p.block_table != nullptr) {
+                        row %= p.page_size;
+                        outer = page * p.Hkv + s.g;
                     }
+                    decode_check_tile(p, row, outer);
+                    const uint32_t dst = sKV + at.e * L::kTileBytes;
+                    for (int kb = 0; kb < L::kKB; ++kb)
+                        tma_load_3d(dst + kb * L::kBlockBytes, map, bar_full(at.e), kb * 64, row, outer);
                 }
                 at.next();
             }

@@ -519,6 +519,9 @@ int attn_decode_kv8_paged(const void* q, const void* k_pages, const void* v_page
  * see itself has its own bit set.  Nodes i >= n_b, and nodes that see no row,
  * get O = 0 and LSE = -inf.  When n < n_b, the rows c + j < 0 do not exist.
  * Rows a node does not see (K, V, NaN included) have no effect on it.
+ * Scores, sums and O are fp32; the softmax weights are rounded to bf16 for the product
+ * with V and normalised by the sum of the rounded ones, as in attn_decode_mq.  bf16
+ * caches only: 8-bit ones are read by attn_decode_kv8.
  *
  *   q          [B, Hq, T, D]        bf16, read
  *   k_cache, v_cache                [B, Hkv, Lmax, D] bf16, read (rows >= seqlens[b] unused)
@@ -636,8 +639,9 @@ int attn_page_release(const int32_t* seqlens, const int32_t* keep_lens, const in
  *   axis_cycle == 0: in blocks, the first sections[0] pairs axis 0, and so on;
  *   axis_cycle != 0: in turn; axis a > 0 has the pairs a, a + n_axes, ..., the
  *                    first sections[a] of them, and axis 0 all others.
- * V and the elements from rot on are not turned.  Angles are exact to about
- * 2e-7 radians at any position; arithmetic is fp32, rounded once.
+ * V and the elements from rot on are not turned.  An angle is off by at most
+ * about 2e-7 + 2^-52 |position inv_freq| radians (at the ends of int32 7e-7 for
+ * inv_freq 1); arithmetic is fp32, rounded once.
  *
  *   q [B, L, Hq, D], k, v [B, L, Hkv, D]  bf16, read; a token's heads are dense, tokens lie
  *                 q_stride, k_stride, v_stride elements apart (multiples of 8), so the three
@@ -692,7 +696,7 @@ int attn_rope_append(const void* q, const void* k, const void* v, long long q_st
  * A length or a path that cannot be moves nothing, leaves the length as it is
  * and flags ATTN_DEVERR_SEQLEN or ATTN_DEVERR_INDEX; rows in a page outside the
  * pool are left out and flag ATTN_DEVERR_PAGE.  D: 64, 128 or 256.  T: 1 .. 1024.
- * Hkv: below 2^24.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ * Hkv: below 2^24.  bf16 caches only.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
  */
 int attn_tree_commit(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seqlens,
                      const int32_t* tree_lens, const int32_t* accept, const int32_t* n_accept, int32_t* out_seqlens,
